@@ -280,6 +280,88 @@ ttt_status ttt_backward_mlp(const void* Q, const void* K, const void* V, const f
                             const void* dZ, float eta, const ttt_shape* s, void* ws, size_t ws_bytes, void* dQ,
                             void* dK, void* dV, float* dWa_out, float* dWb_out, float* deta_out, void* stream);
 
+/* The gated delta rule: test-time training of the linear inner model one token at a time, with a step
+ * size and a forget gate per token (the per-token form of "Vision-TTT" paper notes, section 关键设计 4,
+ * with a gate: G = 0 and Beta = 2 eta is ttt_forward_linear_minibatch with batch_tokens = 1, whose weights
+ * need not be kept per image there).  Per sequence and value head, W [d_v][d_k]:
+ *   W_t = e^{g_t} W_{t-1} + beta_t (v_t - e^{g_t} W_{t-1} k_t) k_t^T,     z_t = scale W_t q_t.
+ * Tensors are ttt_view's: base pointer and element strides of a [batch][heads][tokens][width] tensor
+ * whose width is contiguous, so that buffers laid out by head, by token ([batch][tokens][heads][width]) or
+ * cut out of a larger projection are all passed as they are.
+ *   Q, K: qk_heads heads of width d_k;  V, Z: heads heads of width d_v, dtype (bf16 or fp32).  Value head h
+ *   uses key head h / (heads / qk_heads); heads is a multiple of qk_heads.  d_k, d_v: 64 or 128.
+ *   G (log of the gate, normally <= 0; -inf drops the state), Beta: fp32, one value per token and value
+ *   head (width 1).
+ * Base pointers and strides of the token tensors are multiples of 16 bytes (strides of dimensions of
+ * size 1 are ignored).  Inputs may be broadcast (stride 0) and may share memory; an output may share memory
+ * with nothing else of the call.  Outputs cut from the rows of one buffer (equal token strides, columns
+ * that do not meet) are apart.
+ *   lengths: NULL, or [batch] int32 on the device: sequence b has the first lengths[b] tokens (clamped to
+ *   0 .. tokens).  What lies behind them is neither read nor written. */
+typedef struct {
+    void* data;
+    long long batch_stride, head_stride, token_stride;   /* in elements */
+} ttt_view;
+
+typedef struct {
+    int batch, qk_heads, heads, tokens, d_k, d_v;
+    int dtype;               /* ttt_dtype of Q, K, V, Z and their gradients */
+} ttt_delta_shape;
+
+/* Bytes of device workspace of ttt_forward_gated_delta (backward = 0) or ttt_backward_gated_delta
+ * (backward = 1); 0 for an invalid shape.  It needs no zero fill; calls that may run at the same time
+ * need distinct workspaces.  256-byte aligned. */
+size_t ttt_gated_delta_workspace_bytes(int backward, const ttt_delta_shape* s);
+
+/* Whole sequences.  W0: NULL (zeros), [heads][d_v][d_k] fp32 shared by the batch (w0_shared = 1) or
+ * [batch][heads][d_v][d_k] (w0_shared = 0).  W1_out: optional [batch][heads][d_v][d_k] fp32, the weights
+ * after each sequence's last token.
+ * Chunks of 32 tokens: inside a chunk the token updates are solved together (matrix products), the state goes
+ * from chunk to chunk.  The state is fp32; bf16 tokens are exact operands and everything else is
+ * carried as two bf16 parts (about 16 significant bits), fp32 tokens and everything else as three
+ * (about 24).  Deterministic. */
+ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,
+                                   const ttt_view* Beta, const float* W0, int w0_shared, const int* lengths, float scale,
+                                   const ttt_view* Z, float* W1_out, const ttt_delta_shape* s, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Backward pass of ttt_forward_gated_delta for the upstream gradients dZ (as Z) and dW1 (of W1_out; NULL:
+ * none).  dQ, dK (summed over the value heads that share a key head), dV: like Q, K, V; dG, dBeta: fp32
+ * like G, Beta; dW0_out: optional, like W0 (a shared W0's gradient is summed over the images in order).
+ * The forward pass is run again inside the call.  With D_t the adjoint of W_t (from its token's own readout
+ * and all later tokens), e_t = v_t - e^{g_t} W_{t-1} k_t and y_t = D_t k_t:
+ *   dq_t = scale W_t^T dz_t,  dv_t = beta_t y_t,  dbeta_t = y_t . e_t,
+ *   dk_t = beta_t (D_t^T e_t - e^{g_t} W_{t-1}^T y_t),
+ *   dg_t = < e^{g_t} W_{t-1}, D_t - dv_t k_t^T >,   D_{t-1} = e^{g_t} (D_t - dv_t k_t^T) + scale dz_{t-1} q_{t-1}^T.
+ * Rows of the gradients behind a sequence's length are left as they were.  Deterministic. */
+ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,
+                                    const ttt_view* Beta, const float* W0, int w0_shared, const int* lengths, float scale,
+                                    const ttt_view* dZ, const float* dW1, const ttt_delta_shape* s, void* ws,
+                                    size_t ws_bytes, const ttt_view* dQ, const ttt_view* dK, const ttt_view* dV,
+                                    const ttt_view* dG, const ttt_view* dBeta, float* dW0_out, void* stream);
+
+/* The recurrent form: s->tokens (one, or a few) new tokens of each row of a batch, on a cache of states
+ * W [n_slots][heads][d_v][d_k] fp32 that is updated in place.  slots: [batch] int32 on the device, the
+ * state of each row (NULL: row b uses state b); a row whose slot is outside 0 .. n_slots - 1 is unused: neither
+ * its Z nor any state is written.  Rows that name the same state take their steps in batch order.
+ * fp32 arithmetic; no workspace. */
+ttt_status ttt_step_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,
+                                const ttt_view* Beta, float* W, int n_slots, const int* slots, float scale, const ttt_view* Z,
+                                const ttt_delta_shape* s, void* stream);
+
+/* Clipping by the global norm, of the gradients the backward entry points give: with
+ * norm = sqrt(sum over all n tensors of the squares), out_i = grads_i * min(1, max_norm / norm).
+ *   grads, out, counts, dtypes: host arrays of length n; tensor i has counts[i] >= 0 contiguous elements of
+ *   dtypes[i] (ttt_dtype), aligned to its element size.  out[i] = grads[i] clips in place (nothing is
+ *   written when the norm is at most max_norm); otherwise an output may share memory with nothing else.
+ *   norm_out: one fp32 on the device, the norm before clipping.  max_norm >= 0 (infinity: the norm only,
+ *   outputs are copies).  A NaN norm gives NaN everywhere; an infinite norm scales by zero.
+ *   ws: ttt_clip_workspace_bytes(n) bytes, 256-byte aligned, no zero fill.  Nothing is copied from the host arrays
+ *   after the call returns; a captured call keeps the addresses.  Deterministic. */
+size_t ttt_clip_workspace_bytes(int n);
+ttt_status ttt_clip_gradients(const void* const* grads, void* const* out, const long long* counts, const int* dtypes, int n,
+                              float max_norm, float* norm_out, void* ws, size_t ws_bytes, void* stream);
+
 /* A layer whose heads [0, heads - conv_heads) are linear heads and whose last conv_heads heads are
  * depthwise-conv heads (ViT^3 keeps one conv head among its linear heads: press article,
  * Observation 6), over one [batch][heads][N][d] view described by s (s->heads = all heads):

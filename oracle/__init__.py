@@ -19,6 +19,9 @@ Functions and the definitions they follow (page titles and sections; see ``ttt_o
   linear_backward(...), dwconv_backward(...), mlp_backward(...)
                     the chain rule through the full-batch linear / depthwise-conv / MLP step: dQ, dK,
                     dV, the weights' gradients, deta
+  gated_delta(...), gated_delta_backward(...)
+                    the linear inner model trained one token at a time with a forget gate, token by
+                    token, and its chain rule
   gelu_tanh(u), gelu_tanh_deriv(u), gelu_tanh_deriv2(u)
 
 Parity status: every function here is pinned by tests/test_oracle_pins.py (closed forms,
@@ -47,6 +50,9 @@ def _load():
         lib.oracle_linear_dot.argtypes = [i, i, i, i, dp, dp, dp, dp, d, dp, dp, i]
         lib.oracle_linear_minibatch.argtypes = [i, i, i, i, i, i, dp, dp, dp, dp, d, dp, dp, i]
         lib.oracle_linear_backward.argtypes = [i, i, i, i, dp, dp, dp, dp, d, dp, dp, dp, dp, dp, dp, i]
+        ip = ctypes.POINTER(i)
+        lib.oracle_gated_delta.argtypes = [i] * 6 + [ip] + [dp] * 6 + [i, d, dp, dp, i]
+        lib.oracle_gated_delta_backward.argtypes = [i] * 6 + [ip] + [dp] * 6 + [i, d] + [dp] * 8 + [i]
         lib.oracle_dwconv.argtypes = [i, i, i, i, i, dp, dp, dp, dp, d, dp, dp, i]
         lib.oracle_dwconv_dot.argtypes = [i, i, i, i, i, dp, dp, dp, dp, d, dp, dp, i]
         lib.oracle_conv3x3.argtypes = [i, i, i, i, i, dp, dp, dp, dp, d, dp, dp, i]
@@ -54,7 +60,7 @@ def _load():
         lib.oracle_mlp_backward.argtypes = [i, i, i, i, i, dp, dp, dp, dp, dp, d, dp, dp, dp, dp, dp, dp, dp, i]
         lib.oracle_mlp.argtypes = [i, i, i, i, i, dp, dp, dp, dp, dp, d, dp, dp, dp, i]
         for f in (lib.oracle_linear, lib.oracle_linear_gram, lib.oracle_linear_dot, lib.oracle_linear_minibatch,
-                  lib.oracle_linear_backward,
+                  lib.oracle_linear_backward, lib.oracle_gated_delta, lib.oracle_gated_delta_backward,
                   lib.oracle_dwconv,
                   lib.oracle_dwconv_dot, lib.oracle_conv3x3, lib.oracle_dwconv_backward, lib.oracle_mlp_backward,
                   lib.oracle_mlp):
@@ -240,6 +246,49 @@ def mlp(Q, K, V, Wa, Wb, eta, threads=None):
     _check(_load().oracle_mlp(B, H, N, d, hidden, _p(Q), _p(K), _p(V), _p(Wa), _p(Wb), float(eta),
                               _p(Wa1), _p(Wb1), _p(Z), threads or default_threads()), "mlp")
     return Z, Wa1, Wb1
+
+
+def _gated_delta_inputs(Q, K, V, G, Beta, W0, lengths):
+    Q, K, V, G, Beta = (_f64(x) for x in (Q, K, V, G, Beta))
+    B, hk, N, dk = Q.shape
+    h, dv = V.shape[1], V.shape[3]
+    assert K.shape == Q.shape and V.shape == (B, h, N, dv) and G.shape == Beta.shape == (B, h, N) and h % hk == 0
+    W0 = np.zeros((h, dv, dk)) if W0 is None else _f64(W0)
+    assert W0.shape in ((h, dv, dk), (B, h, dv, dk))
+    if lengths is not None:
+        lengths = np.ascontiguousarray(np.asarray(lengths), dtype=np.int32)
+        assert lengths.shape == (B,) and lengths.min() >= 0 and lengths.max() <= N
+    lp = None if lengths is None else lengths.ctypes.data_as(ctypes.POINTER(ctypes.c_int))
+    return (B, hk, h, N, dk, dv), lengths, lp, Q, K, V, G, Beta, W0, int(W0.ndim == 3)
+
+
+def gated_delta(Q, K, V, G, Beta, W0=None, lengths=None, scale=1.0, threads=None):
+    """Q, K [B][hk][N][dk], V [B][h][N][dv], G (log gates), Beta [B][h][N], W0 None (zeros), [h][dv][dk] or
+    [B][h][dv][dk].  Returns (Z [B][h][N][dv], zeros behind a sequence's length, W1 [B][h][dv][dk])."""
+    n, lengths, lp, Q, K, V, G, Beta, W0, shared = _gated_delta_inputs(Q, K, V, G, Beta, W0, lengths)
+    B, _, h, N, dk, dv = n
+    Z, W1 = np.zeros((B, h, N, dv)), np.empty((B, h, dv, dk))
+    _check(_load().oracle_gated_delta(*n, lp, _p(Q), _p(K), _p(V), _p(G), _p(Beta), _p(W0), shared, float(scale),
+                                      _p(W1), _p(Z), threads or default_threads()), "gated_delta")
+    return Z, W1
+
+
+def gated_delta_backward(Q, K, V, G, Beta, dZ, W0=None, dW1=None, lengths=None, scale=1.0, threads=None):
+    """Returns (dQ, dK summed over the value heads of a key head, dV, dG, dBeta, dW0 like W0 -- per head and image
+    when W0 is None), zeros behind a sequence's length."""
+    n, lengths, lp, Q, K, V, G, Beta, W0, shared = _gated_delta_inputs(Q, K, V, G, Beta, W0, lengths)
+    B, hk, h, N, dk, dv = n
+    dZ = _f64(dZ)
+    assert dZ.shape == (B, h, N, dv)
+    dW1 = None if dW1 is None else _f64(dW1)
+    dQ, dK, dV = np.zeros((B, h, N, dk)), np.zeros((B, h, N, dk)), np.zeros((B, h, N, dv))
+    dG, dBeta, dW0 = np.zeros((B, h, N)), np.zeros((B, h, N)), np.empty((B, h, dv, dk))
+    _check(_load().oracle_gated_delta_backward(*n, lp, _p(Q), _p(K), _p(V), _p(G), _p(Beta), _p(W0), shared, float(scale),
+                                               _p(dZ), None if dW1 is None else _p(dW1), _p(dQ), _p(dK), _p(dV), _p(dG),
+                                               _p(dBeta), _p(dW0), threads or default_threads()),
+           "gated_delta_backward")
+    group = lambda x: x.reshape(B, hk, h // hk, N, dk).sum(2)  # noqa: E731
+    return group(dQ), group(dK), dV, dG, dBeta, dW0.sum(0) if shared else dW0
 
 
 def gelu_tanh(u):

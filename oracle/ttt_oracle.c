@@ -431,6 +431,141 @@ int oracle_linear_minibatch(int B, int heads, int N, int d, int b, int mode, con
 }
 
 /* ------------------------------------------------------------------------------------------ */
+/* Gated delta rule: the linear inner model trained one token at a time, with a step size and a */
+/* forget gate per token ("Vision-TTT" paper notes, section 关键设计 4, with batches of one token */
+/* and a gate):                                                                                 */
+/*   W_t = e^{g_t} W_{t-1} + beta_t (v_t - e^{g_t} W_{t-1} k_t) k_t^T,   z_t = scale W_t q_t.    */
+/* ------------------------------------------------------------------------------------------ */
+
+/* One unit over its first `len` tokens; rows of Z behind them are not written.  W [dv][dk] is updated in place.
+ * With `states` ([len + 1][dv][dk]) and `resid` ([len][dv]), the weights before each token and after the
+ * last, and the residuals, are kept. */
+static void gated_delta_unit(int len, int dk, int dv, const double* Q, const double* K, const double* V, const double* G,
+                             const double* Beta, double scale, double* W, double* Z, double* states, double* resid)
+{
+    const size_t n = (size_t)dv * dk;
+    for (int t = 0; t < len; ++t) {
+        const double *q = Q + (size_t)t * dk, *k = K + (size_t)t * dk, *v = V + (size_t)t * dv;
+        const double fade = exp(G[t]);
+        if (states) memcpy(states + t * n, W, n * sizeof(double));
+        for (int i = 0; i < dv; ++i) {
+            double* w = W + (size_t)i * dk;
+            double pred = 0.0, z = 0.0;
+            for (int j = 0; j < dk; ++j) {
+                w[j] *= fade;
+                pred += w[j] * k[j];
+            }
+            const double e = v[i] - pred;
+            if (resid) resid[(size_t)t * dv + i] = e;
+            for (int j = 0; j < dk; ++j) {
+                w[j] += Beta[t] * e * k[j];
+                z += w[j] * q[j];
+            }
+            Z[(size_t)t * dv + i] = scale * z;
+        }
+    }
+    if (states) memcpy(states + (size_t)len * n, W, n * sizeof(double));
+}
+
+/* Q, K [B][hk][N][dk], V, Z [B][h][N][dv], G, Beta [B][h][N], W0 [h][dv][dk] (w0_shared) or [B][h][dv][dk],
+ * W1 [B][h][dv][dk].  Value head u uses key head u / (h / hk). */
+int oracle_gated_delta(int B, int hk, int h, int N, int dk, int dv, const int* lengths, const double* Q, const double* K,
+                       const double* V, const double* G, const double* Beta, const double* W0, int w0_shared, double scale,
+                       double* W1, double* Z, int nthreads)
+{
+    if (B < 0 || hk < 1 || h < 1 || h % hk || N < 1 || dk < 1 || dv < 1) return ORACLE_ERR_ARG;
+    const size_t n = (size_t)dv * dk;
+    if (nthreads < 1) nthreads = 1;
+#pragma omp parallel for schedule(dynamic, 1) num_threads(nthreads)
+    for (long u = 0; u < (long)B * h; ++u) {
+        const long b = u / h, hv = u % h, ku = b * hk + hv / (h / hk);
+        double* W = W1 + u * n;
+        memcpy(W, W0 + (w0_shared ? hv : u) * n, n * sizeof(double));
+        gated_delta_unit(lengths ? lengths[b] : N, dk, dv, Q + (size_t)ku * N * dk, K + (size_t)ku * N * dk,
+                         V + (size_t)u * N * dv, G + (size_t)u * N, Beta + (size_t)u * N, scale, W, Z + (size_t)u * N * dv,
+                         NULL, NULL);
+    }
+    return ORACLE_OK;
+}
+
+/* One unit's backward pass, token by token from the last.  D [dv][dk] holds the upstream gradient of the last weights
+ * and is left holding the gradient of the first; dq, dk_ [len][dk] are this unit's own (not summed over units). */
+static void gated_delta_backward_unit(int len, int dk, int dv, const double* Q, const double* K, const double* G,
+                                      const double* Beta, double scale, const double* states, const double* resid,
+                                      const double* dZ, double* D, double* dq, double* dkk, double* dvv, double* dg,
+                                      double* dbeta)
+{
+    const size_t n = (size_t)dv * dk;
+    for (int t = len - 1; t >= 0; --t) {
+        const double *q = Q + (size_t)t * dk, *k = K + (size_t)t * dk, *dz = dZ + (size_t)t * dv;
+        const double *before = states + (size_t)t * n, *after = before + n, *e = resid + (size_t)t * dv;
+        const double fade = exp(G[t]);
+        double* dqt = dq + (size_t)t * dk;
+        double* dkt = dkk + (size_t)t * dk;
+        for (int j = 0; j < dk; ++j) dqt[j] = dkt[j] = 0.0;
+        dg[t] = dbeta[t] = 0.0;
+        for (int i = 0; i < dv; ++i) {
+            double* d = D + (size_t)i * dk;
+            double du = 0.0;
+            for (int j = 0; j < dk; ++j) {
+                dqt[j] += scale * after[(size_t)i * dk + j] * dz[i];
+                d[j] += scale * dz[i] * q[j];
+                du += d[j] * k[j];
+            }
+            const double de = Beta[t] * du;                  /* of the residual, hence of v */
+            dvv[(size_t)t * dv + i] = de;
+            dbeta[t] += du * e[i];
+            for (int j = 0; j < dk; ++j) {
+                const double faded = fade * before[(size_t)i * dk + j];
+                dkt[j] += Beta[t] * e[i] * d[j] - de * faded;
+                d[j] -= de * k[j];
+                dg[t] += d[j] * faded;
+                d[j] *= fade;
+            }
+        }
+    }
+}
+
+/* dZ like Z; dW1 [B][h][dv][dk] or NULL.  dQu, dKu [B][h][N][dk] per value head; dV, dG, dBeta like V, G, Beta;
+ * dW0u [B][h][dv][dk].  Rows behind a sequence's length are not written. */
+int oracle_gated_delta_backward(int B, int hk, int h, int N, int dk, int dv, const int* lengths, const double* Q, const double* K,
+                                const double* V, const double* G, const double* Beta, const double* W0, int w0_shared,
+                                double scale, const double* dZ, const double* dW1, double* dQu, double* dKu, double* dV,
+                                double* dG, double* dBeta, double* dW0u, int nthreads)
+{
+    if (B < 0 || hk < 1 || h < 1 || h % hk || N < 1 || dk < 1 || dv < 1) return ORACLE_ERR_ARG;
+    const size_t n = (size_t)dv * dk;
+    int status = ORACLE_OK;
+    if (nthreads < 1) nthreads = 1;
+#pragma omp parallel for schedule(dynamic, 1) num_threads(nthreads)
+    for (long u = 0; u < (long)B * h; ++u) {
+        const long b = u / h, hv = u % h, ku = b * hk + hv / (h / hk);
+        const int len = lengths ? lengths[b] : N;
+        const double *q = Q + (size_t)ku * N * dk, *k = K + (size_t)ku * N * dk;
+        double* W = (double*)malloc(n * sizeof(double));
+        double* Z = (double*)malloc((size_t)N * dv * sizeof(double));
+        double* states = (double*)malloc(((size_t)len + 1) * n * sizeof(double));
+        double* resid = (double*)malloc((size_t)N * dv * sizeof(double));
+        if (W && Z && states && resid) {
+            memcpy(W, W0 + (w0_shared ? hv : u) * n, n * sizeof(double));
+            gated_delta_unit(len, dk, dv, q, k, V + (size_t)u * N * dv, G + (size_t)u * N, Beta + (size_t)u * N, scale, W, Z,
+                             states, resid);
+            double* D = dW0u + u * n;
+            if (dW1) memcpy(D, dW1 + u * n, n * sizeof(double));
+            else memset(D, 0, n * sizeof(double));
+            gated_delta_backward_unit(len, dk, dv, q, k, G + (size_t)u * N, Beta + (size_t)u * N, scale, states, resid,
+                                      dZ + (size_t)u * N * dv, D, dQu + (size_t)u * N * dk, dKu + (size_t)u * N * dk,
+                                      dV + (size_t)u * N * dv, dG + (size_t)u * N, dBeta + (size_t)u * N);
+        } else {
+#pragma omp atomic write
+            status = ORACLE_ERR_NOMEM;
+        }
+        free(W); free(Z); free(states); free(resid);
+    }
+    return status;
+}
+
+/* ------------------------------------------------------------------------------------------ */
 /* 3x3 depthwise-convolution inner model over the H x W token grid                             */
 /* (press article, Observation 6 and Fig. 5 part 3; ViT3 news article, 原則六 and section      */
 /* 效果全面驗證: one head uses a 3x3 depthwise convolution).                                     */

@@ -20,6 +20,8 @@ EXPORTED = (
     "ttt_workspace_bytes", "ttt_workspace_init", "ttt_workspace_status",
     "ttt_forward_linear", "ttt_forward_dwconv", "ttt_forward_conv3x3", "ttt_forward_mlp", "ttt_forward_linear_noalloc", "ttt_noalloc_status",
     "ttt_forward_linear_minibatch", "ttt_backward_linear", "ttt_backward_dwconv", "ttt_backward_mlp",
+    "ttt_gated_delta_workspace_bytes", "ttt_forward_gated_delta", "ttt_backward_gated_delta", "ttt_step_gated_delta",
+    "ttt_clip_workspace_bytes", "ttt_clip_gradients",
     "ttt_layer_workspace_bytes", "ttt_forward_layer", "ttt_selftest_wait_timeout", "ttt_set_wait_limit",
     "ttt_status_string", "ttt_last_error", "ttt_version",
 )
@@ -32,6 +34,16 @@ class TttShape(ctypes.Structure):
         ("batch_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
         ("dtype", ctypes.c_int), ("max_sms", ctypes.c_int), ("loss", ctypes.c_int),
     ]
+
+
+class TttView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong)]
+
+
+class TttDeltaShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("qk_heads", ctypes.c_int), ("heads", ctypes.c_int), ("tokens", ctypes.c_int),
+                ("d_k", ctypes.c_int), ("d_v", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 class TttError(RuntimeError):
@@ -82,6 +94,20 @@ def lib():
         L.ttt_layer_workspace_bytes.restype = sz
         L.ttt_forward_layer.argtypes = [vp, vp, vp, vp, vp, vp, f, shp, i, vp, sz, vp, vp, vp]
         L.ttt_forward_layer.restype = i
+        vw, dshp, pp = ctypes.POINTER(TttView), ctypes.POINTER(TttDeltaShape), ctypes.POINTER(vp)
+        L.ttt_gated_delta_workspace_bytes.argtypes = [i, dshp]
+        L.ttt_gated_delta_workspace_bytes.restype = sz
+        L.ttt_forward_gated_delta.argtypes = [vw] * 5 + [vp, i, vp, f, vw, vp, dshp, vp, sz, vp]
+        L.ttt_forward_gated_delta.restype = i
+        L.ttt_backward_gated_delta.argtypes = [vw] * 5 + [vp, i, vp, f, vw, vp, dshp, vp, sz] + [vw] * 5 + [vp, vp]
+        L.ttt_backward_gated_delta.restype = i
+        L.ttt_step_gated_delta.argtypes = [vw] * 5 + [vp, i, vp, f, vw, dshp, vp]
+        L.ttt_step_gated_delta.restype = i
+        L.ttt_clip_workspace_bytes.argtypes = [i]
+        L.ttt_clip_workspace_bytes.restype = sz
+        L.ttt_clip_gradients.argtypes = [pp, pp, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(i), i, f, vp, vp, sz,
+                                         vp]
+        L.ttt_clip_gradients.restype = i
         L.ttt_selftest_wait_timeout.argtypes = [vp, sz, ctypes.c_ulonglong, vp]
         L.ttt_selftest_wait_timeout.restype = i
         L.ttt_set_wait_limit.argtypes = [ctypes.c_ulonglong]
@@ -171,6 +197,37 @@ def ttt_forward_layer(Q, K, V, W0_lin, W0_conv, Z, eta, shape, conv_heads, ws, w
                       stream):
     return lib().ttt_forward_layer(Q, K, V, W0_lin, W0_conv, Z, eta, ctypes.byref(shape), conv_heads, ws, ws_bytes,
                                    W1_lin_out, W1_conv_out, stream)
+
+
+def make_delta_shape(batch, qk_heads, heads, tokens, d_k, d_v, dtype):
+    return TttDeltaShape(batch, qk_heads, heads, tokens, d_k, d_v, dtype)
+
+
+def ttt_gated_delta_workspace_bytes(backward, shape):
+    return lib().ttt_gated_delta_workspace_bytes(backward, shape)
+
+
+def ttt_forward_gated_delta(Q, K, V, G, Beta, W0, w0_shared, lengths, scale, Z, W1_out, shape, ws, ws_bytes, stream):
+    return lib().ttt_forward_gated_delta(Q, K, V, G, Beta, W0, w0_shared, lengths, scale, Z, W1_out, shape, ws,
+                                         ws_bytes, stream)
+
+
+def ttt_backward_gated_delta(Q, K, V, G, Beta, W0, w0_shared, lengths, scale, dZ, dW1, shape, ws, ws_bytes, dQ, dK, dV,
+                             dG, dBeta, dW0_out, stream):
+    return lib().ttt_backward_gated_delta(Q, K, V, G, Beta, W0, w0_shared, lengths, scale, dZ, dW1, shape, ws, ws_bytes,
+                                          dQ, dK, dV, dG, dBeta, dW0_out, stream)
+
+
+def ttt_step_gated_delta(Q, K, V, G, Beta, W, n_slots, slots, scale, Z, shape, stream):
+    return lib().ttt_step_gated_delta(Q, K, V, G, Beta, W, n_slots, slots, scale, Z, shape, stream)
+
+
+def ttt_clip_workspace_bytes(n):
+    return lib().ttt_clip_workspace_bytes(n)
+
+
+def ttt_clip_gradients(grads, out, counts, dtypes, n, max_norm, norm_out, ws, ws_bytes, stream):
+    return lib().ttt_clip_gradients(grads, out, counts, dtypes, n, max_norm, norm_out, ws, ws_bytes, stream)
 
 
 def ttt_selftest_wait_timeout(ws, ws_bytes, limit_ns, stream):

@@ -102,6 +102,8 @@ SHAPES = [
     (2, 3, 3, 257, 128, 128),
     (1, 1, 2, 1000, 128, 128),
     (40, 2, 2, 5, 64, 64),         # many short sequences
+    (160, 1, 2, 70, 64, 64),       # more tiles of state rows than warps that run at a time
+    (80, 1, 2, 70, 128, 128),
 ]
 
 

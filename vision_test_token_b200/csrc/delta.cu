@@ -129,11 +129,12 @@ __device__ __forceinline__ void put_part(uint8_t* mat, int i, int lane, float x)
 
 template <int DK, int P, int PK, bool BACKWARD>
 __global__ void __launch_bounds__(prep_warps<DK, PK>() * 32)
-delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long total) {
+delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long total, uint32_t* err) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int KP = DK + 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long item = (long long)blockIdx.x * prep_warps<DK, PK>() + warp;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0;
     if (item >= total) return;
     const int c = (int)(item % d.nc);
     const long long bh = item / d.nc;
@@ -229,6 +230,10 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
 // --------------------------------------------------------------------------------------------------
 // Chain
 // --------------------------------------------------------------------------------------------------
+// Two warps share a tile of 16 state rows and two helpers finish it.  With at most one tile per SM a CTA takes one
+// tile, else two, which share the token tiles in shared memory.
+static bool few_tiles(const Dims& d) { return (long long)d.B * d.h * (d.dv / 16) <= 148; }
+
 struct ChainOut {
     View Z;                       // forward: the readout
     float* W1;                    // nullable [B][h][dv][dk]
@@ -237,39 +242,59 @@ struct ChainOut {
     __nv_bfloat16* S;             // backward: states at the groups' starts [B][h][ng][P][dv][dk]
 };
 
-template <int DK, int P, int PK, int NW, bool SAVE>
+// A CTA of a sequential kernel: RT tiles of 16 rows of the state.  Chain warps: KS per tile, each owning DK / KS
+// of the tile's columns.  Helper warps: kHelp per tile, off the sequential path.  One warp loads.
+// The CTA goes from period to period with one barrier each.
+constexpr int kHelp = 2;
+constexpr int kGateSlots = 8;                                  // chunks whose gates are kept in shared memory
+template <int RT, int KS>
+__host__ __device__ constexpr int seq_warps() { return RT * KS + RT * kHelp + 1; }
+
+// Control block of a sequential kernel's CTA.
+struct Ctl {
+    uint64_t full[4];
+    int abort_flag;
+};
+constexpr int kCtlBytes = 64;
+static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
+
+template <int DK, int P, int PK, int RT, int KS, bool SAVE>
 struct ChainLayout {
-    static constexpr int KP = DK + 8;
-    static constexpr int VW = NW * 16;
-    static constexpr int VE = PK == 1 ? 2 : 4;                 // bytes of a value element
-    static constexpr int VP = PK == 1 ? VW + 8 : VW + 4;
-    static constexpr int kK = PK * CT * KP * 2;
+    static constexpr int VW = RT * 16;
+    static constexpr int VB = VW * (PK == 1 ? 2 : 4);          // bytes of a row of the value tile
+    static constexpr int kK = PK * CT * DK * 2;                // K of the period's chunk, then Q of the one before
     static constexpr int kQ = SAVE ? 0 : kK;
-    static constexpr int kV = CT * VP * VE;
-    static constexpr int kR = kGateBytes + (SAVE ? 1 : 2) * mat_bytes(P);
-    static constexpr int stage = kK + kQ + kV + kR;
-    static constexpr int kStages = 3 * stage <= 110 * 1024 ? 3 : 2;
-    static constexpr int warp_out = CT * 24 * 2;               // 32 tokens x 16 values, pitch 24
-    static constexpr int smem = kStages * stage + NW * warp_out;
+    static constexpr int kV = CT * VB;
+    static constexpr int kM = mat_bytes(P);                    // T', then A of the chunk before
+    static constexpr int stage = (kK + kQ + kV + (SAVE ? 1 : 2) * kM + 1023) / 1024 * 1024;
+    static constexpr int kGates = kGateSlots * kGateBytes;
+    static constexpr int kS = DK / 16 * P * 512;               // a tile's state as operand parts
+    static constexpr int kE = 2048;                            // a tile's residuals (or partial sums), fp32
+    static constexpr int kX = KS > 1 ? RT * KS * kE : 0;
+    static constexpr int kOut = RT * kHelp * P * 16 * 48;      // 16 tokens x 16 values per helper and part, pitch 24
+    static constexpr int fixed = kCtlBytes + kGates + 2 * RT * (kS + kE) + kX + kOut + 1024;   // 1024: alignment
+    static constexpr int kStages = 3 * stage + fixed <= 227 * 1024 ? 3 : 2;
+    static constexpr int smem = kStages * stage + fixed;
+    static_assert(VB <= 128 && kK % 1024 == 0 && kV % 1024 == 0, "swizzled tiles");
 };
 
-// One product step of the chain: acc[nb] += (parts a of 16 rows x 16 k) * B, nb = 0..3 (32 columns), B a
-// matrix image [32][MP] with rows = columns of the product (n) and k contiguous; k block kk.
-template <int P>
-__device__ __forceinline__ void mat_nt(float (&acc)[4][4], const uint32_t (&a)[P][4], uint32_t mat, int kk, int lane) {
+// acc (16 x 8) += (parts a of 16 rows x 32 k) * B for one block nb of 8 columns, B a lower-triangular matrix image
+// [32][MP].  NT: B[k][n] = M[n][k] (columns n of the product are M's rows);  else B[k][n] = M[k][n].
+template <int P, int PA, bool NT>
+__device__ __forceinline__ void mat_block(float (&acc)[4], const uint32_t (&a)[2][PA][4], uint32_t mat, int nb, int lane) {
     const int mi = lane >> 3, lr = lane & 7;
 #pragma unroll
-    for (int n2 = kk; n2 < 2; ++n2)                            // lower triangular: columns n >= k
+    for (int pb = 0; pb < P; ++pb) {
+        uint32_t b[4];
+        if (NT) ldsm4(b, mat + ((pb * CT + nb * 8 + lr) * MP + mi * 8) * 2);
+        else ldsm4t(b, mat + ((pb * CT + mi * 8 + lr) * MP + nb * 8) * 2);
 #pragma unroll
-        for (int pb = 0; pb < P; ++pb) {
-            uint32_t b[4];
-            ldsm4(b, mat + ((pb * CT + n2 * 16 + (mi >> 1) * 8 + lr) * MP + kk * 16 + (mi & 1) * 8) * 2);
-#pragma unroll
-            for (int pa = 0; pa + pb < P; ++pa) {
-                mma16816(acc[2 * n2], a[pa], b[0], b[1]);
-                mma16816(acc[2 * n2 + 1], a[pa], b[2], b[3]);
+        for (int pa = 0; pa < PA; ++pa)
+            if (pa + pb < P) {
+                if (NT || nb < 2) mma16816(acc, a[0][pa], b[0], b[1]);
+                if (!NT || nb >= 2) mma16816(acc, a[1][pa], b[2], b[3]);
             }
-        }
+    }
 }
 
 // The parts of accumulator blocks (2 kk, 2 kk + 1) as a left operand for k block kk.
@@ -290,17 +315,23 @@ __device__ __forceinline__ void as_operand(uint32_t (&a)[P][4], const float (&x)
     for (int p = 0; p < P; ++p) a[p][3] = o[p];
 }
 
-// s (16 x DK) += (parts a: 16 x 16 tokens of block kk) * X, X [part][32 tokens][DK + 8].
-template <int DK, int P, int PK>
-__device__ __forceinline__ void add_outer(float (&s)[DK / 8][4], const uint32_t (&a)[P][4], uint32_t x, int kk, int lane) {
-    constexpr int KP = DK + 8;
+// A token tile in shared memory, as TMA writes it: [part][64-feature half][32 tokens][128 bytes], the 16-byte pieces
+// of a row permuted by the row's low bits (128-byte swizzle), so that eight rows' pieces lie in distinct banks.
+template <int DK>
+constexpr int kTilePart = CT * DK * 2;
+
+// s (16 x DW columns from col0) += (parts a: 16 x 16 tokens of block kk) * X, X a token tile.
+template <int DK, int DW, int P, int PK>
+__device__ __forceinline__ void add_outer(float (&s)[DW / 8][4], const uint32_t (&a)[P][4], uint32_t x, int kk, int col0, int lane) {
     const int mi = lane >> 3, lr = lane & 7;
+    const int c16 = col0 / 16;                     // first 16-column block: DW / 16 blocks, aligned to their number
+    const uint32_t base = x + (kk * 16 + (mi & 1) * 8 + lr) * 128 + ((((mi >> 1) ^ lr) << 4) ^ ((c16 & 3) << 5)) + (c16 >> 2) * 4096;
 #pragma unroll
-    for (int n2 = 0; n2 < DK / 16; ++n2)
+    for (int n2 = 0; n2 < DW / 16; ++n2)
 #pragma unroll
         for (int pb = 0; pb < PK; ++pb) {
             uint32_t b[4];
-            ldsm4t(b, x + ((pb * CT + kk * 16 + (mi & 1) * 8 + lr) * KP + n2 * 16 + (mi >> 1) * 8) * 2);
+            ldsm4t(b, (base ^ ((n2 & 3) << 5)) + (n2 >> 2) * 4096 + pb * kTilePart<DK>);
 #pragma unroll
             for (int pa = 0; pa + pb < P; ++pa) {
                 mma16816(s[2 * n2], a[pa], b[0], b[1]);
@@ -309,149 +340,202 @@ __device__ __forceinline__ void add_outer(float (&s)[DK / 8][4], const uint32_t 
         }
 }
 
-// acc (16 x 32 tokens) += (parts a: 16 x 16 features of block kk) * X^T, X [part][32 tokens][DK + 8].
+// acc (16 x 16 tokens, from token 16 n2) += (parts a: 16 x 16 features from col) * X^T, X a token tile.
 template <int DK, int P, int PK>
-__device__ __forceinline__ void dot_tokens(float (&acc)[4][4], const uint32_t (&a)[P][4], uint32_t x, int kk, int lane) {
-    constexpr int KP = DK + 8;
-    const int mi = lane >> 3, lr = lane & 7;
-#pragma unroll
-    for (int n2 = 0; n2 < 2; ++n2)
-#pragma unroll
-        for (int pb = 0; pb < PK; ++pb) {
-            uint32_t b[4];
-            ldsm4(b, x + ((pb * CT + n2 * 16 + (mi >> 1) * 8 + lr) * KP + kk * 16 + (mi & 1) * 8) * 2);
-#pragma unroll
-            for (int pa = 0; pa + pb < P; ++pa) {
-                mma16816(acc[2 * n2], a[pa], b[0], b[1]);
-                mma16816(acc[2 * n2 + 1], a[pa], b[2], b[3]);
-            }
-        }
-}
-
-// 16 rows x 32 tokens held as accumulators -> bf16 rows [token][16] in `stage` (pitch 24) -> global rows.
-__device__ __forceinline__ void put_rows(uint32_t stage, const uint32_t (&w)[8], __nv_bfloat16* dst, long long ts, int left,
-                                         int lane) {
-    const int mi = lane >> 3, lr = lane & 7;
-#pragma unroll
-    for (int n2 = 0; n2 < 2; ++n2)
-        stsm4t(stage + ((n2 * 16 + (mi >> 1) * 8 + lr) * 24 + (mi & 1) * 8) * 2, w[4 * n2], w[4 * n2 + 1], w[4 * n2 + 2],
-               w[4 * n2 + 3]);
-    __syncwarp();
-    uint4 lo, hi;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w) : "r"(stage + lane * 48) : "memory");
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w) : "r"(stage + lane * 48 + 16) : "memory");
-    if (lane < left) {
-        uint4* o = reinterpret_cast<uint4*>(dst + lane * ts);
-        o[0] = lo;
-        o[1] = hi;
-    }
-    __syncwarp();
-}
-
-template <int P>
-__device__ __forceinline__ void put_rows_parts(uint32_t stage, const float (&e)[4][4], __nv_bfloat16* dst, long long ps,
-                                               long long ts, int left, int lane) {
-    uint32_t w[P][8];
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-        uint32_t o[P];
-        split2<P>(e[nb][0], e[nb][1], o);
-#pragma unroll
-        for (int p = 0; p < P; ++p) w[p][2 * nb] = o[p];
-        split2<P>(e[nb][2], e[nb][3], o);
-#pragma unroll
-        for (int p = 0; p < P; ++p) w[p][2 * nb + 1] = o[p];
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) put_rows(stage, w[p], dst + p * ps, ts, left, lane);
-}
-
-// 16 rows x 32 tokens of accumulators -> the rows of a token tensor (bf16, or fp32 written directly:
-// eight lanes hold eight consecutive features, a 32-byte sector).
-template <int PK>
-__device__ __forceinline__ void put_tokens(uint32_t stage, const float (&z)[4][4], char* base, long long off, long long ts, int left,
+__device__ __forceinline__ void dot_tokens(float (&acc0)[4], float (&acc1)[4], const uint32_t (&a)[P][4], uint32_t x, int n2, int c16,
                                            int lane) {
-    if constexpr (PK == 1) {
-        uint32_t w[8];
+    const int mi = lane >> 3, lr = lane & 7;
+    const uint32_t base = x + (n2 * 16 + (mi >> 1) * 8 + lr) * 128 + ((((mi & 1) ^ lr) << 4) ^ ((c16 & 3) << 5)) + (c16 >> 2) * 4096;
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            w[2 * nb] = pack2(z[nb][0], z[nb][1]);
-            w[2 * nb + 1] = pack2(z[nb][2], z[nb][3]);
+    for (int pb = 0; pb < PK; ++pb) {
+        uint32_t b[4];
+        ldsm4(b, base + pb * kTilePart<DK>);
+#pragma unroll
+        for (int pa = 0; pa + pb < P; ++pa) {
+            mma16816(acc0, a[pa], b[0], b[1]);
+            mma16816(acc1, a[pa], b[2], b[3]);
         }
-        put_rows(stage, w, reinterpret_cast<__nv_bfloat16*>(base) + off, ts, left, lane);
+    }
+}
+
+// Byte offset of (row, byte) in a tile of rows of RB bytes (32, 64 or 128) under TMA's swizzle of that width.
+template <int RB>
+__device__ __forceinline__ uint32_t swz(int row, int byte) {
+    const uint32_t o = row * RB + byte;
+    return o ^ (((o >> 7) & (RB / 16 - 1)) << 4);
+}
+
+__device__ __forceinline__ void sts4(uint32_t a, const float (&v)[4]) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ void sts4u(uint32_t a, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ uint4 lds4u(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+// The sum over a tile's KS warps of one block's partials, in warp order ([warp][4 blocks][32 lanes] float4).
+template <int KS>
+__device__ __forceinline__ void sum_partials(float (&x)[4], uint32_t buf, int nb, int lane) {
+    float4 v = lds4(buf + (nb * 32 + lane) * 16);
+#pragma unroll
+    for (int k = 1; k < KS; ++k) {
+        const float4 w = lds4(buf + ((k * 4 + nb) * 32 + lane) * 16);
+        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+    }
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+// Barrier of the KS warps of tile rt.
+template <int KS>
+__device__ __forceinline__ void tile_sync(int rt) {
+    asm volatile("bar.sync %0, %1;" ::"r"(rt + 1), "n"(KS * 32) : "memory");
+}
+
+// Two blocks of 16 rows x 8 tokens (tokens 0 .. 15) -> bf16 rows [token][16] in `stage` (pitch 24) -> global rows.
+__device__ __forceinline__ void put_pair(uint32_t stage, const uint32_t (&w)[4], __nv_bfloat16* dst, long long ts, int left, int lane) {
+    const int mi = lane >> 3, lr = lane & 7;
+    stsm4t(stage + (((mi >> 1) * 8 + lr) * 24 + (mi & 1) * 8) * 2, w[0], w[1], w[2], w[3]);
+    __syncwarp();
+    const uint4 v = lds4u(stage + (lane >> 1) * 48 + (lane & 1) * 16);
+    if ((lane >> 1) < left) *reinterpret_cast<uint4*>(dst + (lane >> 1) * ts + (lane & 1) * 8) = v;
+    __syncwarp();
+}
+// As bf16 parts (x, y: the two blocks' accumulators), each part `ps` elements apart.
+template <int P>
+__device__ __forceinline__ void put_pair_parts(uint32_t stage, const float (&x)[4], const float (&y)[4], __nv_bfloat16* dst,
+                                               long long ps, long long ts, int left, int lane) {
+    uint32_t a[P][4];
+    as_operand<P>(a, x, y);
+#pragma unroll
+    for (int p = 0; p < P; ++p) put_pair(stage + p * 16 * 48, a[p], dst + p * ps, ts, left, lane);
+}
+// As rows of a token tensor (fp32 is written directly: eight lanes hold eight consecutive features, a 32-byte
+// sector).
+template <int PK>
+__device__ __forceinline__ void put_pair_tokens(uint32_t stage, const float (&x)[4], const float (&y)[4], char* base, long long off,
+                                                long long ts, int left, int lane) {
+    if constexpr (PK == 1) {
+        const uint32_t w[4] = {pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(y[0], y[1]), pack2(y[2], y[3])};
+        put_pair(stage, w, reinterpret_cast<__nv_bfloat16*>(base) + off, ts, left, lane);
     } else {
         const int g = lane >> 2, t = lane & 3;
         float* o = reinterpret_cast<float*>(base) + off;
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int tok = nb * 8 + 2 * t + (q & 1);
-                if (tok < left) o[tok * ts + g + (q >> 1) * 8] = z[nb][q];
-            }
+        for (int q = 0; q < 4; ++q) {
+            const int tok = 2 * t + (q & 1);
+            if (tok < left) o[tok * ts + g + (q >> 1) * 8] = x[q];
+            if (tok + 8 < left) o[(tok + 8) * ts + g + (q >> 1) * 8] = y[q];
+        }
     }
 }
 
-// Rows [row0, row0 + 16) of the state [dv][dk] in global memory, as bf16 parts [P][dv][dk].
+// A tile's operand parts in shared memory ([k block][part][lane] of 16 bytes) -> its rows [row0, row0 + 16) of the
+// state in global memory, bf16 parts [P][dv][DK]; helper `z` of kHelp takes every kHelp-th k block.
 template <int DK, int P>
-__device__ __forceinline__ void put_state_parts(const float (&s)[DK / 8][4], __nv_bfloat16* dst, int dv, int row0, int lane) {
+__device__ __forceinline__ void put_state_parts(uint32_t buf, __nv_bfloat16* dst, int dv, int row0, int z, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const long long ps = (long long)dv * DK;
+    for (int kk = z; kk < DK / 16; kk += kHelp)
 #pragma unroll
-    for (int nb = 0; nb < DK / 8; ++nb)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t o[P];
-            split2<P>(s[nb][2 * half], s[nb][2 * half + 1], o);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                *reinterpret_cast<uint32_t*>(dst + p * ps + (long long)(row0 + g + 8 * half) * DK + nb * 8 + 2 * t) = o[p];
+        for (int p = 0; p < P; ++p) {
+            const uint4 a = lds4u(buf + ((kk * P + p) * 32 + lane) * 16);
+            __nv_bfloat16* o = dst + ((long long)p * dv + row0 + g) * DK + kk * 16 + 2 * t;
+            *reinterpret_cast<uint32_t*>(o) = a.x;
+            *reinterpret_cast<uint32_t*>(o + 8 * DK) = a.y;
+            *reinterpret_cast<uint32_t*>(o + 8) = a.z;
+            *reinterpret_cast<uint32_t*>(o + 8 * DK + 8) = a.w;
         }
 }
-template <int DK>
-__device__ __forceinline__ void put_state(const float (&s)[DK / 8][4], float* dst, int row0, int lane) {
+template <int DK, int DW>
+__device__ __forceinline__ void put_state(const float (&s)[DW / 8][4], float* dst, int row0, int col0, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    dst += (long long)(row0 + g) * DK + col0 + 2 * t;
 #pragma unroll
-    for (int nb = 0; nb < DK / 8; ++nb) {
-        *reinterpret_cast<float2*>(dst + (long long)(row0 + g) * DK + nb * 8 + 2 * t) = make_float2(s[nb][0], s[nb][1]);
-        *reinterpret_cast<float2*>(dst + (long long)(row0 + g + 8) * DK + nb * 8 + 2 * t) = make_float2(s[nb][2], s[nb][3]);
+    for (int nb = 0; nb < DW / 8; ++nb) {
+        *reinterpret_cast<float2*>(dst + nb * 8) = make_float2(s[nb][0], s[nb][1]);
+        *reinterpret_cast<float2*>(dst + 8 * DK + nb * 8) = make_float2(s[nb][2], s[nb][3]);
     }
 }
-template <int DK>
-__device__ __forceinline__ void get_state(float (&s)[DK / 8][4], const float* src, int row0, int lane) {
+template <int DK, int DW>
+__device__ __forceinline__ void get_state(float (&s)[DW / 8][4], const float* src, int row0, int col0, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int nb = 0; nb < DK / 8; ++nb) {
+    for (int nb = 0; nb < DW / 8; ++nb) {
         float2 a = make_float2(0.f, 0.f), b = a;
         if (src) {
-            a = *reinterpret_cast<const float2*>(src + (long long)(row0 + g) * DK + nb * 8 + 2 * t);
-            b = *reinterpret_cast<const float2*>(src + (long long)(row0 + g + 8) * DK + nb * 8 + 2 * t);
+            const float* p = src + (long long)(row0 + g) * DK + col0 + 2 * t + nb * 8;
+            a = *reinterpret_cast<const float2*>(p);
+            b = *reinterpret_cast<const float2*>(p + 8 * DK);
         }
         s[nb][0] = a.x; s[nb][1] = a.y; s[nb][2] = b.x; s[nb][3] = b.y;
     }
 }
 
-// 32 rows x W elements of E bytes into shared memory (row pitch in bytes), rows past `left` zero.
-template <int W, int E, int NT>
-__device__ __forceinline__ void load_rows(uint32_t dst, int pitch, const char* src, long long ts_bytes, int left, int tid) {
-    constexpr int CPR = W * E / 16;
+// A tensor the loading warp takes tiles of: its tensor map (5-D: features, tokens, heads, images, parts; a box is
+// 32 tokens of up to 128 bytes), and the plain view behind it.  A broadcast dimension has extent one in the map.
+struct Tiled {
+    CUtensorMap map;
+    const char* p;
+    long long ps, bs, hs, ts;         // strides in elements
+    int hmul, bmul;                   // 0 where the dimension is broadcast
+    int tma;                          // the map is valid
+};
+
+// The loading warp's side of one stage.  Whole chunks come as TMA boxes.  The last, partial chunk of a sequence is
+// copied by the warp itself: rows past the end repeat the last token's (they have a step size of zero and are
+// never written out, so any finite values do; what lies behind the sequence in memory is not read).
+struct Loader {
+    uint64_t* bar;
+    int lane;
+    __device__ __forceinline__ void flat(uint32_t dst, const uint8_t* src, uint32_t bytes) const {
+        if (lane == 0)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                         "r"(bytes), "r"(s32(bar))
+                         : "memory");
+    }
+    // features [col, col + RB / E) of one part of 32 tokens, as a swizzled tile of rows of RB bytes
+    template <int RB, int E>
+    __device__ __forceinline__ void tile(uint32_t dst, const Tiled& x, int part, int b, int head, int tok, int col, int left) const {
+        if (x.tma && left >= CT) {
+            if (lane == 0)
+                asm volatile(
+                    "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+                    "[%2];" ::"r"(dst),
+                    "l"(&x.map), "r"(s32(bar)), "r"(col), "r"(tok), "r"(head * x.hmul), "r"(b * x.bmul), "r"(part)
+                    : "memory");
+            return;
+        }
+        constexpr int CPR = RB / 16;
+        const char* src = x.p + (part * x.ps + b * x.bs + head * x.hs + tok * x.ts + col) * E;
+        uint4 v[CPR];
 #pragma unroll
-    for (int x0 = 0; x0 < CT * CPR; x0 += NT) {
-        const int x = x0 + tid;
-        if (CT * CPR % NT == 0 || x < CT * CPR) {
-            const int row = x / CPR, col = x % CPR;
-            const bool live = row < left;
-            cp16(dst + row * pitch + col * 16, src + (live ? row : 0) * ts_bytes + col * 16, live);
+        for (int i = 0; i < CPR; ++i) {
+            const int row = (i * 32 + lane) / CPR, c = (i * 32 + lane) % CPR;
+            v[i] = *reinterpret_cast<const uint4*>(src + min(row, left - 1) * x.ts * E + c * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < CPR; ++i) {
+            const int row = (i * 32 + lane) / CPR, c = (i * 32 + lane) % CPR;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + swz<RB>(row, c * 16)), "r"(v[i].x), "r"(v[i].y),
+                         "r"(v[i].z), "r"(v[i].w)
+                         : "memory");
         }
     }
-}
-template <int BYTES, int NT>
-__device__ __forceinline__ void load_flat(uint32_t dst, const uint8_t* src, int tid) {
+    // bytes of a tile that arrive by TMA
+    __device__ __forceinline__ static uint32_t bytes(const Tiled& x, int left, uint32_t n) { return x.tma && left >= CT ? n : 0; }
+};
+template <int DK, int PK>
+__device__ __forceinline__ void load_tokens(const Loader& l, uint32_t dst, const Tiled& x, int b, int head, int tok, int left) {
 #pragma unroll
-    for (int x0 = 0; x0 < BYTES / 16; x0 += NT) {
-        const int x = x0 + tid;
-        if (BYTES / 16 % NT == 0 || x < BYTES / 16) cp16(dst + x * 16, src + x * 16, true);
-    }
+    for (int p = 0; p < PK; ++p)
+#pragma unroll
+        for (int c = 0; c < DK; c += 64) l.template tile<128, 2>(dst + p * kTilePart<DK> + c / 64 * 4096, x, p, b, head, tok, c, left);
 }
 
 __device__ __forceinline__ float2 lds2(uint32_t a) {
@@ -465,146 +549,257 @@ __device__ __forceinline__ float lds1(uint32_t a) {
     return v;
 }
 
-template <int DK, int P, int PK, int NW, bool SAVE>
-__global__ void __launch_bounds__(NW * 32)
-delta_chain(Dims d, Parts Q, Parts K, View V, const uint8_t* rec, const float* W0, long long w0_bs, ChainOut out) {
-    using L = ChainLayout<DK, P, PK, NW, SAVE>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int NT = NW * 32, KP = L::KP;
+// Periods c = 0 .. chunks.  In period c the chain warps take chunk c from the state they hold to the next one
+// and leave the state they started from (as operand parts) and the residuals E in shared memory; the helpers finish
+// chunk c - 1 from those: its readout (forward), or E and the state to global memory (backward, SAVE);
+// the loading warp is one or two periods ahead.
+template <int DK, int P, int PK, int RT, int KS, bool SAVE>
+__global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
+delta_chain(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ Tiled K, const __grid_constant__ Tiled V, const uint8_t* rec, const float* W0, long long w0_bs, ChainOut out, uint32_t* err,
+            unsigned long long wait_ns) {
+    using L = ChainLayout<DK, P, PK, RT, KS, SAVE>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
+    constexpr int DW = DK / KS, KB = DW / 16, NBW = 4 / KS, CW = RT * KS, HW = RT * kHelp;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int slices = d.dv / L::VW;
     const int slice = blockIdx.x % slices;
     const int bh = blockIdx.x / slices, b = bh / d.h, h = bh % d.h;
     const int len = seq_len(d, b), nch = (len + CT - 1) / CT;
-    const int v0 = slice * L::VW, row0 = v0 + warp * 16;
-    const uint32_t sb = s32(smem), wout = sb + L::kStages * L::stage + warp * L::warp_out;
-    const int recb = rec_bytes(P, SAVE);
-
-    auto issue = [&](int c) {
-        if (c < nch) {
-            const uint32_t st = sb + (c % L::kStages) * L::stage;
-            const int left = len - c * CT;
-            const long long tok = (long long)c * CT;
-#pragma unroll
-            for (int p = 0; p < PK; ++p) {
-                load_rows<DK, 2, NT>(st + p * CT * KP * 2, KP * 2,
-                                     reinterpret_cast<const char*>(K.p + p * K.ps + b * K.bs + (h / d.r) * K.hs + tok * K.ts),
-                                     K.ts * 2, left, tid);
-                if (!SAVE)
-                    load_rows<DK, 2, NT>(st + L::kK + p * CT * KP * 2, KP * 2,
-                                         reinterpret_cast<const char*>(Q.p + p * Q.ps + b * Q.bs + (h / d.r) * Q.hs + tok * Q.ts),
-                                         Q.ts * 2, left, tid);
-            }
-            load_rows<L::VW, L::VE, NT>(st + L::kK + L::kQ, L::VP * L::VE,
-                                        V.p + (b * V.bs + h * V.hs + tok * V.ts + v0) * L::VE, V.ts * L::VE, left, tid);
-            load_flat<L::kR, NT>(st + L::kK + L::kQ + L::kV, rec + ((long long)bh * d.nc + c) * recb, tid);
-        }
-        cp_commit();
-    };
-
-    float s[DK / 8][4];
+    const int v0 = slice * L::VW;
     const long long state = (long long)d.dv * DK;
-    get_state<DK>(s, W0 ? W0 + b * w0_bs + h * state : nullptr, row0, lane);
-    for (int c = 0; c < L::kStages - 1; ++c) issue(c);
+    const uint32_t sb = s32(smem), gates = sb + L::kStages * L::stage;
+    const uint32_t sbuf = gates + L::kGates, ebuf = sbuf + 2 * RT * L::kS, xbuf = ebuf + 2 * RT * L::kE, obuf = xbuf + L::kX;
+    Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::smem - 1024 - kCtlBytes);
+    auto gate_slot = [&](int c) { return gates + (c & (kGateSlots - 1)) * kGateBytes; };
+    auto stage_of = [&](int c) { return sb + (c % L::kStages) * L::stage; };
 
-    for (int c = 0; c < nch; ++c) {
-        cp_wait<L::kStages - 2>();
-        __syncthreads();
-        issue(c + L::kStages - 1);
-        const uint32_t st = sb + (c % L::kStages) * L::stage;
-        const uint32_t kt = st, qt = st + L::kK, vt = st + L::kK + L::kQ, gt = vt + L::kV, tm = gt + kGateBytes,
-                       am = tm + mat_bytes(P);
-        const int left = len - c * CT;
-
-        if (SAVE && (c * CT) % d.gt == 0)
-            put_state_parts<DK, P>(s, out.S + ((long long)bh * d.ng + (c * CT) / d.gt) * P * state, d.dv, row0, lane);
-
-        float x[4][4] = {}, z[4][4] = {};
+    if (warp == CW + HW) {
+        // ---------------------------------------------------------------- loads
+        const int recb = rec_bytes(P, SAVE);
+        const Abort ab{&ctl.abort_flag, err, wait_ns};
+        if (lane == 0) {
+            ctl.abort_flag = 0;
+            for (int i = 0; i < L::kStages; ++i) mbar_init(&ctl.full[i], 1);
+            fence_barrier_init();
+        }
+        __syncwarp();
+        auto loads_in = [&](int c) { return c < nch || (!SAVE && c == nch && nch > 0); };
+        auto issue = [&](int c) {
+            if (!loads_in(c)) return;
+            const uint32_t st = stage_of(c);
+            const uint8_t* r = rec + ((long long)bh * d.nc + c) * recb;
+            const Loader l{&ctl.full[c % L::kStages], lane};
+            const bool now = c < nch, before = !SAVE && c >= 1;
+            const int left = len - c * CT;
+            if (lane == 0) {
+                fence_proxy_async_smem();             // the warp's own stores to the stage, before the copies' writes
+                uint32_t n = 0;
+                if (now) n += Loader::bytes(K, left, L::kK) + Loader::bytes(V, left, L::kV) + kGateBytes + L::kM;
+                if (before) n += Loader::bytes(Q, left + CT, L::kK) + L::kM;
+                mbar_arrive_expect_tx(l.bar, n);
+            }
+            __syncwarp();
+            if (now) {
+                load_tokens<DK, PK>(l, st, K, b, h / d.r, c * CT, left);
+                l.template tile<L::VB, PK == 1 ? 2 : 4>(st + L::kK + L::kQ, V, 0, b, h, c * CT, v0, left);
+                l.flat(gate_slot(c), r, kGateBytes);
+                l.flat(st + L::kK + L::kQ + L::kV, r + kGateBytes, L::kM);
+            }
+            if (before) {
+                load_tokens<DK, PK>(l, st + L::kK, Q, b, h / d.r, c * CT - CT, left + CT);
+                l.flat(st + L::kK + L::kQ + L::kV + L::kM, r - recb + kGateBytes + L::kM, L::kM);
+            }
+        };
+        for (int c = 0; c < L::kStages - 1; ++c) issue(c);
+        for (int c = 0; c <= nch; ++c) {
+            if (loads_in(c)) mbar_wait(&ctl.full[c % L::kStages], (c / L::kStages) & 1, ab);
+            __syncthreads();
+            issue(c + L::kStages - 1);
+        }
+        return;
+    }
+    if (warp >= CW) {
+        // ---------------------------------------------------------------- helpers
+        const int hw = warp - CW, rt = hw % RT, z = hw / RT, row0 = v0 + rt * 16;
+        const uint32_t stagebuf = obuf + hw * P * 16 * 48;
+        for (int c = 0; c <= nch; ++c) {
+            __syncthreads();
+            if (c == 0) continue;
+            const int pc = c - 1, left = len - pc * CT;
+            const uint32_t sp = sbuf + ((pc & 1) * RT + rt) * L::kS, ep = ebuf + ((pc & 1) * RT + rt) * L::kE, gt = gate_slot(pc);
+            if constexpr (SAVE) {
+                const float4 v = lds4(ep + (2 * z * 32 + lane) * 16), w = lds4(ep + ((2 * z + 1) * 32 + lane) * 16);
+                const float e0[4] = {v.x, v.y, v.z, v.w}, e1[4] = {w.x, w.y, w.z, w.w};
+                put_pair_parts<P>(stagebuf, e0, e1, out.E + ((long long)bh * d.N + (long long)pc * CT + z * 16) * d.dv + row0, out.e_ps,
+                                  d.dv, left - z * 16, lane);
+                if ((pc * CT) % d.gt == 0)
+                    put_state_parts<DK, P>(sp, out.S + ((long long)bh * d.ng + (pc * CT) / d.gt) * P * state, d.dv, row0, z, lane);
+            } else {
+                // Z of tokens [16 z, 16 z + 16) = scale gamma (Q W^T) + A U
+                const uint32_t st = stage_of(c), qt = st + L::kK, am = st + L::kK + L::kQ + L::kV + L::kM;
+                float acc[2][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
+                for (int kk = 0; kk < DK / 16; ++kk) {
+                    uint32_t a[P][4];
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const uint4 v = lds4u(sp + ((kk * P + p) * 32 + lane) * 16);
+                        a[p][0] = v.x; a[p][1] = v.y; a[p][2] = v.z; a[p][3] = v.w;
+                    }
+                    dot_tokens<DK, P, PK>(acc[0], acc[1], a, qt, z, kk, lane);
+                }
+                uint32_t u[2][P][4];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    float e[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 v = lds4(ep + ((2 * kk + i) * 32 + lane) * 16);
+                        const float2 be = lds2(gt + (2 * CT + (2 * kk + i) * 8 + 2 * t) * 4);
+                        e[i][0] = be.x * v.x; e[i][1] = be.y * v.y; e[i][2] = be.x * v.z; e[i][3] = be.y * v.w;
+                    }
+                    as_operand<P>(u[kk], e[0], e[1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int nb = 2 * z + i;
+                    const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
+                    acc[i][0] *= d.scale * ga.x; acc[i][1] *= d.scale * ga.y; acc[i][2] *= d.scale * ga.x; acc[i][3] *= d.scale * ga.y;
+                    mat_block<P, P, true>(acc[i], u, am, nb, lane);
+                }
+                put_pair_tokens<PK>(stagebuf, acc[0], acc[1], out.Z.p,
+                                    b * out.Z.bs + h * out.Z.hs + ((long long)pc * CT + z * 16) * out.Z.ts + row0, out.Z.ts, left - z * 16, lane);
+            }
+        }
+        return;
+    }
+    // -------------------------------------------------------------------- chain
+    const int ks = warp % KS, rt = warp / KS, col0 = ks * DW, row0 = v0 + rt * 16;
+    const uint32_t xp = xbuf + rt * KS * L::kE;
+    float s[DW / 8][4];
+    get_state<DK, DW>(s, W0 ? W0 + b * w0_bs + h * state : nullptr, row0, col0, lane);
+    for (int c = 0; c <= nch; ++c) {
+        __syncthreads();
+        if (c == nch) break;
+        const uint32_t st = stage_of(c), kt = st, vt = st + L::kK + L::kQ, tm = vt + L::kV, gt = gate_slot(c);
+        const uint32_t sp = sbuf + ((c & 1) * RT + rt) * L::kS, ep = ebuf + ((c & 1) * RT + rt) * L::kE;
+        const bool hand = !SAVE || (c * CT) % d.gt == 0;
+
+        float x[4][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < KB; ++kk) {
             uint32_t a[P][4];
             as_operand<P>(a, s[2 * kk], s[2 * kk + 1]);
-            dot_tokens<DK, P, PK>(x, a, kt, kk, lane);
-            if (!SAVE) dot_tokens<DK, P, PK>(z, a, qt, kk, lane);
+#pragma unroll
+            for (int n2 = 0; n2 < 2; ++n2) dot_tokens<DK, P, PK>(x[2 * n2], x[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
+            if (hand) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) sts4u(sp + (((ks * KB + kk) * P + p) * 32 + lane) * 16, a[p]);
+            }
+        }
+        if constexpr (KS > 1) {
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) sts4(xp + ((ks * 4 + nb) * 32 + lane) * 16, x[nb]);
+            tile_sync<KS>(rt);
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) sum_partials<KS>(x[nb], xp, nb, lane);
         }
         // R = V - gamma (W K^T)
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
-            float v[4];
+        for (int n2 = 0; n2 < 2; ++n2) {
+            float v[2][4];
             if constexpr (PK == 1) {
-                if (nb % 2 == 0) {
-                    uint32_t r[4];
-                    const int mi = lane >> 3, lr = lane & 7;
-                    ldsm4t(r, vt + ((nb * 8 + (mi >> 1) * 8 + lr) * L::VP + warp * 16 + (mi & 1) * 8) * 2);
-                    x[nb][0] = fmaf(-ga.x, x[nb][0], lo_f(r[0]));
-                    x[nb][1] = fmaf(-ga.y, x[nb][1], hi_f(r[0]));
-                    x[nb][2] = fmaf(-ga.x, x[nb][2], lo_f(r[1]));
-                    x[nb][3] = fmaf(-ga.y, x[nb][3], hi_f(r[1]));
-                    const float2 gb = lds2(gt + (nb * 8 + 8 + 2 * t) * 4);
-                    x[nb + 1][0] = fmaf(-gb.x, x[nb + 1][0], lo_f(r[2]));
-                    x[nb + 1][1] = fmaf(-gb.y, x[nb + 1][1], hi_f(r[2]));
-                    x[nb + 1][2] = fmaf(-gb.x, x[nb + 1][2], lo_f(r[3]));
-                    x[nb + 1][3] = fmaf(-gb.y, x[nb + 1][3], hi_f(r[3]));
+                uint32_t r[4];
+                const int mi = lane >> 3, lr = lane & 7;
+                ldsm4t(r, vt + swz<L::VB>(n2 * 16 + (mi >> 1) * 8 + lr, rt * 32 + (mi & 1) * 16));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i >> 1][2 * (i & 1)] = lo_f(r[i]);
+                    v[i >> 1][2 * (i & 1) + 1] = hi_f(r[i]);
                 }
             } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = lds1(vt + ((nb * 8 + 2 * t + (q & 1)) * L::VP + warp * 16 + g + (q >> 1) * 8) * 4);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[nb][q] = fmaf(-((q & 1) ? ga.y : ga.x), x[nb][q], v[q]);
+                    for (int q = 0; q < 4; ++q)
+                        v[i][q] = lds1(vt + swz<L::VB>(n2 * 16 + i * 8 + 2 * t + (q & 1), (rt * 16 + g + (q >> 1) * 8) * 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int nb = 2 * n2 + i;
+                const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[nb][q] = fmaf(-((q & 1) ? ga.y : ga.x), x[nb][q], v[i][q]);
             }
         }
         // E = T' R
         float e[4][4] = {};
+        uint32_t a[2][P][4];
+        as_operand<P>(a[0], x[0], x[1]);
+        as_operand<P>(a[1], x[2], x[3]);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            uint32_t a[P][4];
-            as_operand<P>(a, x[2 * kk], x[2 * kk + 1]);
-            mat_nt<P>(e, a, tm, kk, lane);
-        }
-        if constexpr (SAVE)
-            put_rows_parts<P>(wout, e, out.E + ((long long)bh * d.N + (long long)c * CT) * d.dv + row0, out.e_ps, d.dv, left, lane);
-        // U = beta E, then gamma_C W + (suffix U)^T K
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            const float2 be = lds2(gt + (2 * CT + nb * 8 + 2 * t) * 4);
-            e[nb][0] *= be.x; e[nb][1] *= be.y; e[nb][2] *= be.x; e[nb][3] *= be.y;
-            if (!SAVE) {
-                const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
-                z[nb][0] *= d.scale * ga.x; z[nb][1] *= d.scale * ga.y; z[nb][2] *= d.scale * ga.x; z[nb][3] *= d.scale * ga.y;
-            }
-        }
-        if (!SAVE) {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                uint32_t a[P][4];
-                as_operand<P>(a, e[2 * kk], e[2 * kk + 1]);
-                mat_nt<P>(z, a, am, kk, lane);
-            }
-        }
+        for (int nb = 0; nb < 4; ++nb) mat_block<P, P, true>(e[nb], a, tm, nb, lane);
+        // W <- gamma_C W + (suffix beta E)^T K
         const float gc = lds1(gt + (CT - 1) * 4);
 #pragma unroll
-        for (int nb = 0; nb < DK / 8; ++nb)
+        for (int nb = 0; nb < DW / 8; ++nb)
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[nb][q] *= gc;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
-            const float2 su = lds2(gt + (CT + nb * 8 + 2 * t) * 4);
-            e[nb][0] *= su.x; e[nb][1] *= su.y; e[nb][2] *= su.x; e[nb][3] *= su.y;
+            if (nb / NBW == ks) sts4(ep + (nb * 32 + lane) * 16, e[nb]);
+            const float2 su = lds2(gt + (CT + nb * 8 + 2 * t) * 4), be = lds2(gt + (2 * CT + nb * 8 + 2 * t) * 4);
+            const float u0 = su.x * be.x, u1 = su.y * be.y;
+            e[nb][0] *= u0; e[nb][1] *= u1; e[nb][2] *= u0; e[nb][3] *= u1;
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            uint32_t a[P][4];
-            as_operand<P>(a, e[2 * kk], e[2 * kk + 1]);
-            add_outer<DK, P, PK>(s, a, kt, kk, lane);
+            as_operand<P>(a[kk], e[2 * kk], e[2 * kk + 1]);
+            add_outer<DK, DW, P, PK>(s, a[kk], kt, kk, col0, lane);
         }
-        if (!SAVE)
-            put_tokens<PK>(wout, z, out.Z.p, b * out.Z.bs + h * out.Z.hs + (long long)c * CT * out.Z.ts + row0, out.Z.ts, left, lane);
     }
-    cp_wait<0>();
-    if (out.W1) put_state<DK>(s, out.W1 + (long long)bh * state, row0, lane);
+    if (out.W1) put_state<DK, DW>(s, out.W1 + (long long)bh * state, row0, col0, lane);
 }
+
+// The tensor map of a [part][batch][heads][tokens][width] tensor with boxes of 32 tokens x rb bytes.
+static Tiled tiled(const void* p, long long ps, int parts, long long bs, long long hs, long long ts, const Dims& d, int heads, int width,
+                   int esz, int rb) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                               CUtensorMapFloatOOBfill);
+    static const Encode enc = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Encode>(f) : nullptr;
+    }();
+    Tiled x{};
+    x.p = static_cast<const char*>(p);
+    x.ps = ps; x.bs = bs; x.hs = hs; x.ts = ts;
+    x.hmul = hs != 0;
+    x.bmul = bs != 0;
+    // a dimension of size one keeps a stride that is valid
+    const long long row = (long long)width;
+    const cuuint64_t dims[5] = {(cuuint64_t)width, (cuuint64_t)d.N, (cuuint64_t)(hs ? heads : 1), (cuuint64_t)(bs ? d.B : 1),
+                                (cuuint64_t)parts};
+    const cuuint64_t strides[4] = {(cuuint64_t)(ts ? ts : row) * esz, (cuuint64_t)(hs ? hs : row) * esz, (cuuint64_t)(bs ? bs : row) * esz,
+                                   (cuuint64_t)(ps ? ps : row) * esz};
+    const cuuint32_t box[5] = {(cuuint32_t)(rb / esz), CT, 1, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+    bool ok = enc != nullptr && (ts != 0 || d.N == 1);
+    for (cuuint64_t st : strides) ok = ok && st < (1ull << 40);
+    x.tma = ok && enc(&x.map, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5, const_cast<void*>(p), dims,
+                      strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return x;
+}
+static Tiled tiled(const Parts& x, int parts, const Dims& d, int heads, int width, int rb) {
+    return tiled(x.p, x.ps, parts, x.bs, x.hs, x.ts, d, heads, width, 2, rb);
+}
+
+static uint32_t* error_word(const Call& c) { return reinterpret_cast<uint32_t*>(c.ws); }
 
 #include "delta_backward.cuh"
 
@@ -617,7 +812,7 @@ struct Layout {
 static Layout layout(const Dims& d, bool fp32, bool backward) {
     const int P = fp32 ? 3 : 2;
     Layout l{};
-    size_t at = 0;
+    size_t at = kWsHeader;
     auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
     const size_t heads = (size_t)d.B * d.h, toks = heads * d.N;
     l.rec = take(heads * d.nc * rec_bytes(P, backward));
@@ -664,20 +859,27 @@ static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_
     ttt_status st = check_launch(allow_smem(k, smem));
     if (st != TTT_OK) return st;
     const long long total = (long long)c.d.B * c.d.h * c.d.nc;
-    k<<<(unsigned)((total + kPrepWarps - 1) / kPrepWarps), kPrepWarps * 32, smem, c.stream>>>(c.d, Q, K, c.G, c.Beta, rec, total);
+    k<<<(unsigned)((total + kPrepWarps - 1) / kPrepWarps), kPrepWarps * 32, smem, c.stream>>>(c.d, Q, K, c.G, c.Beta, rec, total,
+                                                                                                     error_word(c));
     return check_launch(cudaGetLastError());
 }
 
-template <int DK, int P, int PK, bool SAVE>
-static ttt_status run_chain(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
-    constexpr int NW = 4;
-    using L = ChainLayout<DK, P, PK, NW, SAVE>;
+template <int DK, int P, int PK, int RT, int KS, bool SAVE>
+static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
+    using L = ChainLayout<DK, P, PK, RT, KS, SAVE>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a chain CTA");
-    auto* k = delta_chain<DK, P, PK, NW, SAVE>;
+    auto* k = delta_chain<DK, P, PK, RT, KS, SAVE>;
     ttt_status st = check_launch(allow_smem(k, L::smem));
     if (st != TTT_OK) return st;
-    k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), NW * 32, L::smem, c.stream>>>(c.d, Q, K, c.V, rec, c.W0, c.w0_bs, out);
+    const Tiled q = tiled(Q, PK, c.d, c.d.hk, DK, 128), kk = tiled(K, PK, c.d, c.d.hk, DK, 128);
+    const Tiled v = tiled(c.V.p, 0, 1, c.V.bs, c.V.hs, c.V.ts, c.d, c.d.h, c.d.dv, PK == 1 ? 2 : 4, L::VB);
+    k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), seq_warps<RT, KS>() * 32, L::smem, c.stream>>>(c.d, q, kk, v, rec, c.W0, c.w0_bs, out, error_word(c),
+                                                                                                             c.wait_ns);
     return check_launch(cudaGetLastError());
+}
+template <int DK, int P, int PK, bool SAVE>
+static ttt_status run_chain(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
+    return few_tiles(c.d) ? run_chain_t<DK, P, PK, 1, 2, SAVE>(c, Q, K, rec, out) : run_chain_t<DK, P, PK, 2, 2, SAVE>(c, Q, K, rec, out);
 }
 
 template <int DK, int P, int PK>

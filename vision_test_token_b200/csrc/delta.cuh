@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "sm100.cuh"
 #include "ttt_internal.h"
 
 namespace ttt {
@@ -51,8 +52,9 @@ struct Call {
     const float* dW1;                 // nullable (backward)
     View dQ, dK, dV, dG, dBeta;
     float* dW0;                       // nullable: dW0 of the layout of W0
-    uint8_t* ws;
+    uint8_t* ws;                      // starts with a header whose first word is the error word
     cudaStream_t stream;
+    unsigned long long wait_ns;       // bound of every device-side wait (ns)
 };
 
 size_t forward_ws_bytes(const Dims& d, bool fp32);

@@ -199,6 +199,7 @@ ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const t
     c.w0_bs = w0_shared ? 0 : state / 4;
     c.W1_out = W1_out;
     c.ws = static_cast<uint8_t*>(ws);
+    c.wait_ns = wait_limit_ns();
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_forward(c);
 }
@@ -245,6 +246,7 @@ ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const 
     c.dW1 = dW1;
     c.dW0 = dW0_out;
     c.ws = static_cast<uint8_t*>(ws);
+    c.wait_ns = wait_limit_ns();
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_backward(c);
 }

@@ -23,173 +23,242 @@ struct BackOut {
     float* dW0;                   // nullable [B][h][dv][dk]
 };
 
-// As mat_nt with the image's rows along k: acc[n = column j] += a (k = row i) * M[i][j], i >= j blocks only.
-template <int P, int PA>
-__device__ __forceinline__ void mat_nn(float (&acc)[4][4], const uint32_t (&a)[PA][4], uint32_t mat, int kk, int lane) {
-    const int mi = lane >> 3, lr = lane & 7;
-#pragma unroll
-    for (int n2 = 0; n2 <= kk; ++n2)
-#pragma unroll
-        for (int pb = 0; pb < P; ++pb) {
-            uint32_t b[4];
-            ldsm4t(b, mat + ((pb * CT + kk * 16 + (mi & 1) * 8 + lr) * MP + n2 * 16 + (mi >> 1) * 8) * 2);
-#pragma unroll
-            for (int pa = 0; pa < PA; ++pa)
-                if (pa + pb < P) {
-                    mma16816(acc[2 * n2], a[pa], b[0], b[1]);
-                    mma16816(acc[2 * n2 + 1], a[pa], b[2], b[3]);
-                }
-        }
-}
-
-template <int DK, int P, int PK, int NW>
+template <int DK, int P, int PK, int RT, int KS>
 struct ReverseLayout {
-    static constexpr int KP = DK + 8, VW = NW * 16, VP = VW + 8;
-    static constexpr int kK = PK * CT * KP * 2;
-    static constexpr int kO = PK * CT * VP * 2;
-    static constexpr int kR = kGateBytes + 2 * mat_bytes(P);
-    static constexpr int stage = 2 * kK + kO + kR;
-    static constexpr int kStages = 3 * stage <= 110 * 1024 ? 3 : 2;
-    static constexpr int warp_out = CT * 24 * 2;
-    static constexpr int smem = kStages * stage + NW * warp_out;
+    static constexpr int VW = RT * 16, VB = VW * 2;
+    static constexpr int kK = PK * CT * DK * 2;                // K, Q and T_u of the period's chunk,
+    static constexpr int kO1 = CT * VB, kO = PK * kO1;         // dZ and A of the next one
+    static constexpr int kM = mat_bytes(P);
+    static constexpr int stage = (2 * kK + kO + 2 * kM + 1023) / 1024 * 1024;
+    static constexpr int kGates = kGateSlots * kGateBytes;
+    static constexpr int kS = DK / 16 * P * 512;               // a tile's adjoint as operand parts
+    static constexpr int kE = 2048;                            // Y, A^T dZ, partial sums
+    static constexpr int kF = 2 * P * 512;                     // scale gamma dZ as operand parts
+    static constexpr int kX = KS > 1 ? RT * KS * kE : 0;
+    static constexpr int kOut = RT * kHelp * P * 16 * 48;
+    static constexpr int fixed = kCtlBytes + kGates + 2 * RT * (kS + 2 * kE + kF) + kX + kOut + 1024;
+    static constexpr int kStages = 3 * stage + fixed <= 227 * 1024 ? 3 : 2;
+    static constexpr int smem = kStages * stage + fixed;
+    static_assert(VB <= 128 && kK % 1024 == 0 && kO1 % 1024 == 0, "swizzled tiles");
 };
 
-template <int DK, int P, int PK, int NW>
-__global__ void __launch_bounds__(NW * 32)
-delta_reverse(Dims d, Parts Q, Parts K, Parts O, const uint8_t* rec, const float* dW1, BackOut out) {
-    using L = ReverseLayout<DK, P, PK, NW>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int NT = NW * 32, KP = L::KP;
+// Periods k = -1 .. chunks, chunks counted from the last.  In period k the chain warps take chunk k; the helpers
+// prepare what chunk k + 1 needs of dZ alone (A^T dZ, and scale gamma dZ as operand parts) and write what chunk
+// k - 1 gave (Y, dV, and the adjoint it started from).
+template <int DK, int P, int PK, int RT, int KS>
+__global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
+delta_reverse(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ Tiled K, const __grid_constant__ Tiled O, const uint8_t* rec, const float* dW1, BackOut out, uint32_t* err,
+              unsigned long long wait_ns) {
+    using L = ReverseLayout<DK, P, PK, RT, KS>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
+    constexpr int DW = DK / KS, KB = DW / 16, NBW = 4 / KS, CW = RT * KS, HW = RT * kHelp;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3;
     const int slices = d.dv / L::VW;
     const int slice = blockIdx.x % slices;
     const int bh = blockIdx.x / slices, b = bh / d.h, h = bh % d.h;
     const int len = seq_len(d, b), nch = (len + CT - 1) / CT;
-    const int v0 = slice * L::VW, row0 = v0 + warp * 16;
-    const uint32_t sb = s32(smem), wout = sb + L::kStages * L::stage + warp * L::warp_out;
-    const int recb = rec_bytes(P, true);
-
-    auto issue = [&](int k) {                     // k-th chunk from the end
-        const int c = nch - 1 - k;
-        if (c >= 0) {
-            const uint32_t st = sb + (k % L::kStages) * L::stage;
-            const int left = len - c * CT;
-            const long long tok = (long long)c * CT;
-#pragma unroll
-            for (int p = 0; p < PK; ++p) {
-                load_rows<DK, 2, NT>(st + p * CT * KP * 2, KP * 2,
-                                     reinterpret_cast<const char*>(K.p + p * K.ps + b * K.bs + (h / d.r) * K.hs + tok * K.ts),
-                                     K.ts * 2, left, tid);
-                load_rows<DK, 2, NT>(st + L::kK + p * CT * KP * 2, KP * 2,
-                                     reinterpret_cast<const char*>(Q.p + p * Q.ps + b * Q.bs + (h / d.r) * Q.hs + tok * Q.ts),
-                                     Q.ts * 2, left, tid);
-                load_rows<L::VW, 2, NT>(st + 2 * L::kK + p * CT * L::VP * 2, L::VP * 2,
-                                        reinterpret_cast<const char*>(O.p + p * O.ps + b * O.bs + h * O.hs + tok * O.ts + v0),
-                                        O.ts * 2, left, tid);
-            }
-            const uint8_t* r = rec + ((long long)bh * d.nc + c) * recb;
-            load_flat<kGateBytes, NT>(st + 2 * L::kK + L::kO, r, tid);
-            load_flat<2 * mat_bytes(P), NT>(st + 2 * L::kK + L::kO + kGateBytes, r + kGateBytes + mat_bytes(P), tid);
-        }
-        cp_commit();
-    };
-
-    float s[DK / 8][4];
+    const int v0 = slice * L::VW;
     const long long state = (long long)d.dv * DK;
-    get_state<DK>(s, dW1 ? dW1 + bh * state : nullptr, row0, lane);
-    for (int k = 0; k < L::kStages - 1; ++k) issue(k);
+    const uint32_t sb = s32(smem), gates = sb + L::kStages * L::stage;
+    const uint32_t sbuf = gates + L::kGates, ybuf = sbuf + 2 * RT * L::kS, abuf = ybuf + 2 * RT * L::kE, fbuf = abuf + 2 * RT * L::kE,
+                   xbuf = fbuf + 2 * RT * L::kF, obuf = xbuf + L::kX;
+    Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::smem - 1024 - kCtlBytes);
+    auto gate_slot = [&](int k) { return gates + (k & (kGateSlots - 1)) * kGateBytes; };
+    auto stage_of = [&](int k) { return sb + ((k + 1) % L::kStages) * L::stage; };
 
-    for (int k = 0; k < nch; ++k) {
-        const int c = nch - 1 - k;
-        cp_wait<L::kStages - 2>();
+    if (warp == CW + HW) {
+        // ---------------------------------------------------------------- loads
+        const int recb = rec_bytes(P, true);
+        const Abort ab{&ctl.abort_flag, err, wait_ns};
+        if (lane == 0) {
+            ctl.abort_flag = 0;
+            for (int i = 0; i < L::kStages; ++i) mbar_init(&ctl.full[i], 1);
+            fence_barrier_init();
+        }
+        __syncwarp();
+        auto issue = [&](int k) {
+            if (k >= nch) return;
+            const uint32_t st = stage_of(k);
+            const Loader l{&ctl.full[(k + 1) % L::kStages], lane};
+            const bool now = k >= 0, next = k + 1 < nch;
+            if (!now && !next) return;
+            const int c = nch - 1 - k;                // the chunk of this period; the next one is c - 1
+            if (lane == 0) {
+                fence_proxy_async_smem();             // the warp's own stores to the stage, before the copies' writes
+                uint32_t n = 0;
+                if (now) n += Loader::bytes(K, len - c * CT, L::kK) + Loader::bytes(Q, len - c * CT, L::kK) + L::kM;
+                if (next) n += Loader::bytes(O, len - (c - 1) * CT, L::kO) + kGateBytes + L::kM;
+                mbar_arrive_expect_tx(l.bar, n);
+            }
+            __syncwarp();
+            if (now) {
+                load_tokens<DK, PK>(l, st, K, b, h / d.r, c * CT, len - c * CT);
+                load_tokens<DK, PK>(l, st + L::kK, Q, b, h / d.r, c * CT, len - c * CT);
+                l.flat(st + 2 * L::kK + L::kO, rec + ((long long)bh * d.nc + c) * recb + kGateBytes + 2 * L::kM, L::kM);
+            }
+            if (next) {
+                const uint8_t* r = rec + ((long long)bh * d.nc + c - 1) * recb;
+#pragma unroll
+                for (int p = 0; p < PK; ++p)
+                    l.template tile<L::VB, 2>(st + 2 * L::kK + p * L::kO1, O, p, b, h, (c - 1) * CT, v0, len - (c - 1) * CT);
+                l.flat(gate_slot(k + 1), r, kGateBytes);
+                l.flat(st + 2 * L::kK + L::kO + L::kM, r + kGateBytes + L::kM, L::kM);
+            }
+        };
+        for (int k = -1; k < L::kStages - 2; ++k) issue(k);
+        for (int k = -1; k <= nch; ++k) {
+            if (k < nch && nch > 0) mbar_wait(&ctl.full[(k + 1) % L::kStages], ((k + 1) / L::kStages) & 1, ab);
+            __syncthreads();
+            issue(k + L::kStages - 1);
+        }
+        return;
+    }
+    if (warp >= CW) {
+        // ---------------------------------------------------------------- helpers
+        const int hw = warp - CW, rt = hw % RT, z = hw / RT, row0 = v0 + rt * 16;
+        const uint32_t stagebuf = obuf + hw * P * 16 * 48;
+        for (int k = -1; k <= nch; ++k) {
+            __syncthreads();
+            if (k + 1 < nch) {
+                const int n = k + 1, mi = lane >> 3, lr = lane & 7;
+                const uint32_t st = stage_of(k), ot = st + 2 * L::kK, am = ot + L::kO + L::kM, gt = gate_slot(n);
+                uint32_t o[2][PK][4];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int p = 0; p < PK; ++p)
+                        ldsm4t(o[kk][p], ot + p * L::kO1 + swz<L::VB>(kk * 16 + (mi >> 1) * 8 + lr, rt * 32 + (mi & 1) * 16));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float acc[4] = {};
+                    mat_block<P, PK, false>(acc, o, am, 2 * z + i, lane);
+                    sts4(abuf + ((n & 1) * RT + rt) * L::kE + ((2 * z + i) * 32 + lane) * 16, acc);
+                }
+                // tokens 16 z + 2t (+1), then + 8; none behind the end of the sequence
+                float f[2][4];
+                const int tl = len - (nch - 1 - n) * CT - z * 16 - 2 * t;
+                const float2 g0 = lds2(gt + (z * 16 + 2 * t) * 4), g1 = lds2(gt + (z * 16 + 8 + 2 * t) * 4);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float lo = 0.f, hi = 0.f;
+#pragma unroll
+                    for (int p = PK - 1; p >= 0; --p) {
+                        const uint32_t w = z ? o[1][p][q] : o[0][p][q];
+                        lo += lo_f(w);
+                        hi += hi_f(w);
+                    }
+                    f[q >> 1][2 * (q & 1)] = 8 * (q >> 1) < tl ? lo * (d.scale * ((q >> 1) ? g1.x : g0.x)) : 0.f;
+                    f[q >> 1][2 * (q & 1) + 1] = 8 * (q >> 1) + 1 < tl ? hi * (d.scale * ((q >> 1) ? g1.y : g0.y)) : 0.f;
+                }
+                uint32_t a[P][4];
+                as_operand<P>(a, f[0], f[1]);
+#pragma unroll
+                for (int p = 0; p < P; ++p) sts4u(fbuf + ((n & 1) * RT + rt) * L::kF + ((z * P + p) * 32 + lane) * 16, a[p]);
+            }
+            if (k >= 1) {
+                const int n = k - 1, c = nch - 1 - n, left = len - c * CT;
+                const uint32_t yp = ybuf + ((n & 1) * RT + rt) * L::kE, gt = gate_slot(n);
+                const float4 v = lds4(yp + (2 * z * 32 + lane) * 16), w = lds4(yp + ((2 * z + 1) * 32 + lane) * 16);
+                const float y0[4] = {v.x, v.y, v.z, v.w}, y1[4] = {w.x, w.y, w.z, w.w};
+                put_pair_parts<P>(stagebuf, y0, y1, out.Y + ((long long)bh * d.N + (long long)c * CT + z * 16) * d.dv + row0, out.y_ps,
+                                  d.dv, left - z * 16, lane);
+                const float2 b0 = lds2(gt + (2 * CT + z * 16 + 2 * t) * 4), b1 = lds2(gt + (2 * CT + z * 16 + 8 + 2 * t) * 4);
+                const float d0[4] = {b0.x * v.x, b0.y * v.y, b0.x * v.z, b0.y * v.w};
+                const float d1[4] = {b1.x * w.x, b1.y * w.y, b1.x * w.z, b1.y * w.w};
+                put_pair_tokens<PK>(stagebuf, d0, d1, out.dV.p,
+                                    b * out.dV.bs + h * out.dV.hs + ((long long)c * CT + z * 16) * out.dV.ts + row0, out.dV.ts, left - z * 16,
+                                    lane);
+                if (n == 0 || ((c + 1) * CT) % d.gt == 0)
+                    put_state_parts<DK, P>(sbuf + ((n & 1) * RT + rt) * L::kS,
+                                           out.D + ((long long)bh * d.ng + (c * CT) / d.gt) * P * state, d.dv, row0, z, lane);
+            }
+        }
+        return;
+    }
+    // -------------------------------------------------------------------- chain
+    const int ks = warp % KS, rt = warp / KS, col0 = ks * DW, row0 = v0 + rt * 16;
+    const uint32_t xp = xbuf + rt * KS * L::kE;
+    float s[DW / 8][4];
+    get_state<DK, DW>(s, dW1 ? dW1 + bh * state : nullptr, row0, col0, lane);
+    for (int k = -1; k <= nch; ++k) {
         __syncthreads();
-        issue(k + L::kStages - 1);
-        const uint32_t st = sb + (k % L::kStages) * L::stage;
-        const uint32_t kt = st, qt = st + L::kK, ot = st + 2 * L::kK, gt = ot + L::kO, am = gt + kGateBytes, um = am + mat_bytes(P);
-        const int left = len - c * CT;
-        if (k == 0 || ((c + 1) * CT) % d.gt == 0)
-            put_state_parts<DK, P>(s, out.D + ((long long)bh * d.ng + (c * CT) / d.gt) * P * state, d.dv, row0, lane);
+        if (k < 0 || k >= nch) continue;
+        const int c = nch - 1 - k;
+        const uint32_t st = stage_of(k), kt = st, qt = st + L::kK, um = st + 2 * L::kK + L::kO, gt = gate_slot(k);
+        const uint32_t sp = sbuf + ((k & 1) * RT + rt) * L::kS, yp = ybuf + ((k & 1) * RT + rt) * L::kE,
+                       ap = abuf + ((k & 1) * RT + rt) * L::kE, fp = fbuf + ((k & 1) * RT + rt) * L::kF;
+        const bool hand = k == 0 || ((c + 1) * CT) % d.gt == 0;
 
+        // dU = suffix (D K^T) + A^T dZ
         float x[4][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
+        for (int kk = 0; kk < KB; ++kk) {
             uint32_t a[P][4];
             as_operand<P>(a, s[2 * kk], s[2 * kk + 1]);
-            dot_tokens<DK, P, PK>(x, a, kt, kk, lane);
-        }
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            const float2 su = lds2(gt + (CT + nb * 8 + 2 * t) * 4);
-            x[nb][0] *= su.x; x[nb][1] *= su.y; x[nb][2] *= su.x; x[nb][3] *= su.y;
+            for (int n2 = 0; n2 < 2; ++n2) dot_tokens<DK, P, PK>(x[2 * n2], x[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
+            if (hand) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) sts4u(sp + (((ks * KB + kk) * P + p) * 32 + lane) * 16, a[p]);
+            }
         }
-        // dU += dZ^T A;   the scaled dZ' as the left operand of the state's update
+        if constexpr (KS > 1) {
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) sts4(xp + ((ks * 4 + nb) * 32 + lane) * 16, x[nb]);
+        }
+        // D <- gamma_C D + (scale gamma dZ)^T Q
         const float gc = lds1(gt + (CT - 1) * 4);
 #pragma unroll
-        for (int nb = 0; nb < DK / 8; ++nb)
+        for (int nb = 0; nb < DW / 8; ++nb)
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[nb][q] *= gc;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            uint32_t o[PK][4];
-            const int mi = lane >> 3, lr = lane & 7;
-#pragma unroll
-            for (int p = 0; p < PK; ++p)
-                ldsm4t(o[p], ot + ((p * CT + kk * 16 + (mi >> 1) * 8 + lr) * L::VP + warp * 16 + (mi & 1) * 8) * 2);
-            mat_nn<P, PK>(x, o, am, kk, lane);
-            float f[2][4];                        // tokens kk 16 + 2t (+1), then + 8
-            const float2 g0 = lds2(gt + (kk * 16 + 2 * t) * 4), g1 = lds2(gt + (kk * 16 + 8 + 2 * t) * 4);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                f[0][2 * q] = lo_f(o[0][q]);
-                f[0][2 * q + 1] = hi_f(o[0][q]);
-                f[1][2 * q] = lo_f(o[0][2 + q]);
-                f[1][2 * q + 1] = hi_f(o[0][2 + q]);
-#pragma unroll
-                for (int p = 1; p < PK; ++p) {
-                    f[0][2 * q] += lo_f(o[p][q]);
-                    f[0][2 * q + 1] += hi_f(o[p][q]);
-                    f[1][2 * q] += lo_f(o[p][2 + q]);
-                    f[1][2 * q + 1] += hi_f(o[p][2 + q]);
-                }
-                f[0][2 * q] *= d.scale * g0.x;
-                f[0][2 * q + 1] *= d.scale * g0.y;
-                f[1][2 * q] *= d.scale * g1.x;
-                f[1][2 * q + 1] *= d.scale * g1.y;
-            }
             uint32_t a[P][4];
-            as_operand<P>(a, f[0], f[1]);
-            add_outer<DK, P, PK>(s, a, qt, kk, lane);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const uint4 v = lds4u(fp + ((kk * P + p) * 32 + lane) * 16);
+                a[p][0] = v.x; a[p][1] = v.y; a[p][2] = v.z; a[p][3] = v.w;
+            }
+            add_outer<DK, DW, P, PK>(s, a, qt, kk, col0, lane);
+        }
+        if constexpr (KS > 1) {
+            tile_sync<KS>(rt);
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) sum_partials<KS>(x[nb], xp, nb, lane);
+        }
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+            const float2 su = lds2(gt + (CT + nb * 8 + 2 * t) * 4);
+            const float4 v = lds4(ap + (nb * 32 + lane) * 16);
+            x[nb][0] = fmaf(su.x, x[nb][0], v.x);
+            x[nb][1] = fmaf(su.y, x[nb][1], v.y);
+            x[nb][2] = fmaf(su.x, x[nb][2], v.z);
+            x[nb][3] = fmaf(su.y, x[nb][3], v.w);
         }
         // Y = T_u^T dU
         float y[4][4] = {};
+        uint32_t a[2][P][4];
+        as_operand<P>(a[0], x[0], x[1]);
+        as_operand<P>(a[1], x[2], x[3]);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            uint32_t a[P][4];
-            as_operand<P>(a, x[2 * kk], x[2 * kk + 1]);
-            mat_nn<P, P>(y, a, um, kk, lane);
-        }
-        put_rows_parts<P>(wout, y, out.Y + ((long long)bh * d.N + (long long)c * CT) * d.dv + row0, out.y_ps, d.dv, left, lane);
-        // dV = beta Y;   D -= (gamma dV)^T K
+        for (int nb = 0; nb < 4; ++nb) mat_block<P, P, false>(y[nb], a, um, nb, lane);
+        // D -= (gamma beta Y)^T K
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
-            const float2 be = lds2(gt + (2 * CT + nb * 8 + 2 * t) * 4);
-            y[nb][0] *= be.x; y[nb][1] *= be.y; y[nb][2] *= be.x; y[nb][3] *= be.y;
-        }
-        put_tokens<PK>(wout, y, out.dV.p, b * out.dV.bs + h * out.dV.hs + (long long)c * CT * out.dV.ts + row0, out.dV.ts, left, lane);
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
-            y[nb][0] *= -ga.x; y[nb][1] *= -ga.y; y[nb][2] *= -ga.x; y[nb][3] *= -ga.y;
+            if (nb / NBW == ks) sts4(yp + (nb * 32 + lane) * 16, y[nb]);
+            const float2 be = lds2(gt + (2 * CT + nb * 8 + 2 * t) * 4), ga = lds2(gt + (nb * 8 + 2 * t) * 4);
+            const float u0 = -ga.x * be.x, u1 = -ga.y * be.y;
+            y[nb][0] *= u0; y[nb][1] *= u1; y[nb][2] *= u0; y[nb][3] *= u1;
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            uint32_t a[P][4];
-            as_operand<P>(a, y[2 * kk], y[2 * kk + 1]);
-            add_outer<DK, P, PK>(s, a, kt, kk, lane);
+            as_operand<P>(a[kk], y[2 * kk], y[2 * kk + 1]);
+            add_outer<DK, DW, P, PK>(s, a[kk], kt, kk, col0, lane);
         }
     }
-    cp_wait<0>();
-    if (out.dW0) put_state<DK>(s, out.dW0 + bh * state, row0, lane);
+    if (out.dW0) put_state<DK, DW>(s, out.dW0 + bh * state, row0, col0, lane);
 }
 
 // --------------------------------------------------------------------------------------------------
@@ -602,16 +671,23 @@ static ttt_status run_sum_images(const float* part, float* out, int B, long long
     return check_launch(cudaGetLastError());
 }
 
-template <int DK, int P, int PK>
-static ttt_status run_reverse(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const BackOut& out) {
-    constexpr int NW = 4;
-    using L = ReverseLayout<DK, P, PK, NW>;
+template <int DK, int P, int PK, int RT, int KS>
+static ttt_status run_reverse_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const BackOut& out) {
+    using L = ReverseLayout<DK, P, PK, RT, KS>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a reverse CTA");
-    auto* k = delta_reverse<DK, P, PK, NW>;
+    auto* k = delta_reverse<DK, P, PK, RT, KS>;
     ttt_status st = check_launch(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem));
     if (st != TTT_OK) return st;
-    k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), NW * 32, L::smem, c.stream>>>(c.d, Q, K, O, rec, c.dW1, out);
+    const Tiled q = tiled(Q, PK, c.d, c.d.hk, DK, 128), kk = tiled(K, PK, c.d, c.d.hk, DK, 128), o = tiled(O, PK, c.d, c.d.h, c.d.dv, L::VB);
+    k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), seq_warps<RT, KS>() * 32, L::smem, c.stream>>>(c.d, q, kk, o, rec, c.dW1, out, error_word(c),
+                                                                                                             c.wait_ns);
     return check_launch(cudaGetLastError());
+}
+template <int DK, int P, int PK>
+static ttt_status run_reverse(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const BackOut& out) {
+    // fp32: the three parts of a second tile do not fit the shared memory
+    if (PK == 3 || few_tiles(c.d)) return run_reverse_t<DK, P, PK, 1, 2>(c, Q, K, O, rec, out);
+    return run_reverse_t<DK, P, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out);
 }
 
 template <int DK, int P, int PK, bool GROUP>

@@ -1,21 +1,25 @@
-"""Build libttt.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc.
+"""Build libttt.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and the CPython binding _native.so.
 
     python -m vision_test_token_b200.build [--force]
 
 Every .cu file under csrc/ is compiled with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and linked, with the static CUDA runtime,
-into ``vision_test_token_b200/libttt.so``.  No torch headers or libraries are involved.
+into ``vision_test_token_b200/libttt.so``.  No torch headers or libraries are involved in that.
+csrc/native.cpp (the fast marshalling of torch tensors for the per-token entries) is compiled with g++ against
+torch's headers into ``vision_test_token_b200/_native.so``, which links to libttt.so.
 """
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libttt.so")
+NATIVE = os.path.join(PKG, "_native.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -37,9 +41,9 @@ def _deps():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(OUT):
+    if not force and os.path.exists(OUT) and os.path.exists(NATIVE):
         newest = max(os.path.getmtime(f) for f in _deps())
-        if os.path.getmtime(OUT) >= newest:
+        if min(os.path.getmtime(OUT), os.path.getmtime(NATIVE)) >= newest:
             return OUT
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -65,7 +69,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = OUT + ".tmp"
     subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], check=True)
     os.replace(tmp, OUT)
+    _build_native()
     return OUT
+
+
+def _build_native():
+    import torch                                # its headers and libraries; the import is slow, hence here
+    root = os.path.dirname(torch.__file__)
+    include = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), sysconfig.get_paths()["include"]]
+    tmp = NATIVE + ".tmp"
+    subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include),
+                    os.path.join(CSRC, "native.cpp"), "-o", tmp, "-L", PKG, "-l:libttt.so", "-L", os.path.join(root, "lib"),
+                    "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, NATIVE)
 
 
 if __name__ == "__main__":

@@ -26,6 +26,7 @@
 // Bound: the chain of chunks (per chunk and warp about 300 matrix instructions at d = 128, issued one per
 // 8 cycles per SM quarter: the instruction's rate here was measured at 1,009 multiply-adds per cycle and SM).
 #include <algorithm>
+#include <atomic>
 
 #include "delta.cuh"
 
@@ -799,6 +800,19 @@ static Tiled tiled(const Parts& x, int parts, const Dims& d, int heads, int widt
     return tiled(x.p, x.ps, parts, x.bs, x.hs, x.ts, d, heads, width, 2, rb);
 }
 
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device (set once per kernel and device).
+template <auto kernel>
+static ttt_status allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};            // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return check_launch(e);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return TTT_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return check_launch(e);
+}
+
 static uint32_t* error_word(const Call& c) { return reinterpret_cast<uint32_t*>(c.ws); }
 
 #include "delta_backward.cuh"
@@ -837,10 +851,6 @@ size_t backward_ws_bytes(const Dims& d, bool fp32) { return layout(d, fp32, true
 // --------------------------------------------------------------------------------------------------
 // Launches
 // --------------------------------------------------------------------------------------------------
-template <class F>
-static cudaError_t allow_smem(F* kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
 
 // The tokens of x as bf16 parts: x itself (bf16), or 3 parts in the workspace (fp32).
 static Parts as_parts(const View& x, bool fp32, uint8_t* ws, const Dims& d, int heads, int width, cudaStream_t st) {
@@ -855,8 +865,8 @@ static Parts as_parts(const View& x, bool fp32, uint8_t* ws, const Dims& d, int 
 template <int DK, int P, int PK, bool BACKWARD>
 static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_t* rec) {
     constexpr int kPrepWarps = prep_warps<DK, PK>(), smem = kPrepWarps * prep_warp_bytes<DK, PK>();
-    auto* k = delta_prep<DK, P, PK, BACKWARD>;
-    ttt_status st = check_launch(allow_smem(k, smem));
+    constexpr auto k = delta_prep<DK, P, PK, BACKWARD>;
+    ttt_status st = allow_smem<k>(smem);
     if (st != TTT_OK) return st;
     const long long total = (long long)c.d.B * c.d.h * c.d.nc;
     k<<<(unsigned)((total + kPrepWarps - 1) / kPrepWarps), kPrepWarps * 32, smem, c.stream>>>(c.d, Q, K, c.G, c.Beta, rec, total,
@@ -868,8 +878,8 @@ template <int DK, int P, int PK, int RT, int KS, bool SAVE>
 static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
     using L = ChainLayout<DK, P, PK, RT, KS, SAVE>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a chain CTA");
-    auto* k = delta_chain<DK, P, PK, RT, KS, SAVE>;
-    ttt_status st = check_launch(allow_smem(k, L::smem));
+    constexpr auto k = delta_chain<DK, P, PK, RT, KS, SAVE>;
+    ttt_status st = allow_smem<k>(L::smem);
     if (st != TTT_OK) return st;
     const Tiled q = tiled(Q, PK, c.d, c.d.hk, DK, 128), kk = tiled(K, PK, c.d, c.d.hk, DK, 128);
     const Tiled v = tiled(c.V.p, 0, 1, c.V.bs, c.V.hs, c.V.ts, c.d, c.d.h, c.d.dv, PK == 1 ? 2 : 4, L::VB);

@@ -675,8 +675,8 @@ template <int DK, int P, int PK, int RT, int KS>
 static ttt_status run_reverse_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const BackOut& out) {
     using L = ReverseLayout<DK, P, PK, RT, KS>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a reverse CTA");
-    auto* k = delta_reverse<DK, P, PK, RT, KS>;
-    ttt_status st = check_launch(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem));
+    constexpr auto k = delta_reverse<DK, P, PK, RT, KS>;
+    ttt_status st = allow_smem<k>(L::smem);
     if (st != TTT_OK) return st;
     const Tiled q = tiled(Q, PK, c.d, c.d.hk, DK, 128), kk = tiled(K, PK, c.d, c.d.hk, DK, 128), o = tiled(O, PK, c.d, c.d.h, c.d.dv, L::VB);
     k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), seq_warps<RT, KS>() * 32, L::smem, c.stream>>>(c.d, q, kk, o, rec, c.dW1, out, error_word(c),
@@ -694,8 +694,8 @@ template <int DK, int P, int PK, bool GROUP>
 static ttt_status run_grads_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo) {
     using L = GradsLayout<DK, P, PK>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a gradient CTA");
-    auto* k = delta_grads<DK, P, PK, GROUP>;
-    ttt_status st = check_launch(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem));
+    constexpr auto k = delta_grads<DK, P, PK, GROUP>;
+    ttt_status st = allow_smem<k>(L::smem);
     if (st != TTT_OK) return st;
     k<<<(unsigned)((long long)c.d.B * c.d.hk * c.d.ng), 256, L::smem, c.stream>>>(c.d, Q, K, O, c.G, c.Beta, fo.E, bo.Y, fo.e_ps,
                                                                                  fo.S, bo.D, c.dQ, c.dK, c.dG, c.dBeta);

@@ -26,6 +26,7 @@
 // Bound: the chain of chunks (per chunk and warp about 300 matrix instructions at d = 128, issued one per
 // 8 cycles per SM quarter: the instruction's rate here was measured at 1,009 multiply-adds per cycle and SM).
 #include <algorithm>
+#include <array>
 #include <atomic>
 
 #include "delta.cuh"
@@ -65,8 +66,12 @@ __host__ __device__ constexpr int prep_warps() { return PK == 1 ? 4 : 2; }
 
 template <int DK, int PK>
 __host__ __device__ constexpr int prep_tile_bytes() { return PK * CT * (DK + 8) * 2; }
-template <int DK, int PK>
-__host__ __device__ constexpr int prep_warp_bytes() { return 2 * prep_tile_bytes<DK, PK>() + 2 * CT * GP * 4; }
+// A warp's shared memory: the K and Q tiles, then, in their place, the two fp32 matrices and one matrix image.
+template <int DK, int P, int PK>
+__host__ __device__ constexpr int prep_warp_bytes() {
+    constexpr int tiles = 2 * prep_tile_bytes<DK, PK>(), after = 2 * CT * GP * 4 + mat_bytes(P);
+    return tiles > after ? tiles : after;
+}
 
 // 32 tokens x 32 tokens of X Y^T over DK features; X, Y [part][32][DK + 8].  Two 16-row tiles.
 template <int DK, int PK>
@@ -117,14 +122,39 @@ __device__ __forceinline__ void put32(float* dst, const float (&c)[2][4][4], int
         }
 }
 
-// Row i, column `lane` of a bf16 part image.
+// The warp's matrix image in shared memory -> global memory.
+template <int P>
+__device__ __forceinline__ void copy_image(uint8_t* dst, const uint8_t* image, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int x = lane; x < mat_bytes(P) / 16; x += 32) reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(image)[x];
+    __syncwarp();
+}
+// init - g . y[0 .. i), g row i of a 32 x 32 fp32 matrix in shared memory (four sums at a time; i is a constant once
+// the caller's loop is unrolled).
+__device__ __forceinline__ float row_dot(float init, const float* g, const float (&y)[CT], int i) {
+    float s[4] = {init, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int l = 0; l < CT; l += 4) {
+        if (l >= i) continue;
+        const float4 v = *reinterpret_cast<const float4*>(g + l);
+        s[0] = fmaf(-v.x, y[l], s[0]);
+        if (l + 1 < i) s[1] = fmaf(-v.y, y[l + 1], s[1]);
+        if (l + 2 < i) s[2] = fmaf(-v.z, y[l + 2], s[2]);
+        if (l + 3 < i) s[3] = fmaf(-v.w, y[l + 3], s[3]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Row i, column `lane` of a bf16 part image.  (Rounded as a pair: the conversion of a single value runs at an eighth
+// of that rate and was what this kernel waited for.)
 template <int P>
 __device__ __forceinline__ void put_part(uint8_t* mat, int i, int lane, float x) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const __nv_bfloat16 v = __float2bfloat16_rn(x);
-        reinterpret_cast<__nv_bfloat16*>(mat)[(p * CT + i) * MP + lane] = v;
-        x -= __bfloat162float(v);
+        const uint32_t w = pack2(x, 0.f);
+        reinterpret_cast<uint16_t*>(mat)[(p * CT + i) * MP + lane] = (uint16_t)w;
+        x -= lo_f(w);
     }
 }
 
@@ -142,10 +172,11 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
     const int h = (int)(bh % d.h), b = (int)(bh / d.h);
     const int left = seq_len(d, b) - c * CT;
     if (left <= 0) return;
-    uint8_t* my = smem + warp * prep_warp_bytes<DK, PK>();
+    uint8_t* my = smem + warp * prep_warp_bytes<DK, P, PK>();
     const uint32_t kt = s32(my), qt = kt + prep_tile_bytes<DK, PK>();
-    float* kkm = reinterpret_cast<float*>(my + 2 * prep_tile_bytes<DK, PK>());
+    float* kkm = reinterpret_cast<float*>(my);
     float* qkm = kkm + CT * GP;
+    uint8_t* image = my + 2 * CT * GP * 4;
     {
         const long long ko = b * K.bs + (h / d.r) * K.hs + (long long)c * CT * K.ts;
         const long long qo = b * Q.bs + (h / d.r) * Q.hs + (long long)c * CT * Q.ts;
@@ -184,47 +215,44 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
     cp_wait<0>();
     __syncwarp();
     {
-        float m[2][4][4];
+        float m[2][4][4], w[2][4][4];
         gram32<DK, PK>(m, kt, kt, lane);
+        gram32<DK, PK>(w, qt, kt, lane);
+        __syncwarp();                                  // the tiles have been read: the matrices take their place
         put32(kkm, m, lane);
-        gram32<DK, PK>(m, qt, kt, lane);
-        put32(qkm, m, lane);
+        put32(qkm, w, lane);
     }
     __syncwarp();
     // column `lane` (= j): Gamma_ij with its log summed from zero at i = j
     uint8_t* Tm = out + kGateBytes;
-    uint8_t* Am = Tm + mat_bytes(P);
-    uint8_t* Um = Am + mat_bytes(P);
     float s = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < CT; ++i) {
         const float gi = __shfl_sync(~0u, g, i);
         s = i > lane ? s + gi : 0.f;
-        const float dec = i >= lane ? expf(s) : 0.f;
-        const float a = i >= lane ? d.scale * dec * qkm[i * GP + lane] : 0.f;
-        put_part<P>(Am, i, lane, a);
+        // bf16 tokens: the fast exponential, relative error about 2^-22 (1 + |s|)
+        const float dec = i < lane ? 0.f : PK == 1 ? __expf(s) : expf(s);
+        put_part<P>(image, i, lane, i >= lane ? d.scale * dec * qkm[i * GP + lane] : 0.f);
         kkm[i * GP + lane] = i > lane ? dec * kkm[i * GP + lane] : 0.f;
     }
-    __syncwarp();
+    copy_image<P>(Tm + mat_bytes(P), image, lane);
+    // forward substitution, one column per lane
     float y[CT];
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
-        float x = i == lane ? 1.f : 0.f;
-#pragma unroll
-        for (int l = 0; l < i; ++l) x = fmaf(-kkm[i * GP + l], y[l], x);
-        put_part<P>(Tm, i, lane, x);
+        const float x = row_dot(i == lane ? 1.f : 0.f, kkm + i * GP, y, i);
+        put_part<P>(image, i, lane, x);
         y[i] = x * __shfl_sync(~0u, beta, i);
     }
+    copy_image<P>(Tm, image, lane);
     if constexpr (BACKWARD) {
 #pragma unroll
         for (int i = 0; i < CT; ++i) {
-            float a = 0.f;
-#pragma unroll
-            for (int l = 0; l < i; ++l) a = fmaf(kkm[i * GP + l], y[l], a);
-            const float x = (i == lane ? 1.f : 0.f) - __shfl_sync(~0u, beta, i) * a;
-            put_part<P>(Um, i, lane, x);
+            const float x = (i == lane ? 1.f : 0.f) + __shfl_sync(~0u, beta, i) * row_dot(0.f, kkm + i * GP, y, i);
+            put_part<P>(image, i, lane, x);
             y[i] = x;
         }
+        copy_image<P>(Tm + 2 * mat_bytes(P), image, lane);
     }
 }
 
@@ -763,9 +791,10 @@ delta_chain(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ Til
     if (out.W1) put_state<DK, DW>(s, out.W1 + (long long)bh * state, row0, col0, lane);
 }
 
-// The tensor map of a [part][batch][heads][tokens][width] tensor with boxes of 32 tokens x rb bytes.
-static Tiled tiled(const void* p, long long ps, int parts, long long bs, long long hs, long long ts, const Dims& d, int heads, int width,
-                   int esz, int rb) {
+// A five-dimensional tensor map: boxes of `rows` along the second dimension x rb bytes (32, 64 or 128, swizzled alike)
+// along the first.  strides: elements, of dimensions 1 .. 4.
+static bool encode_map(CUtensorMap* m, const void* p, int esz, std::array<cuuint64_t, 5> dims, std::array<long long, 4> strides, int rb,
+                       int rows) {
     typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                CUtensorMapFloatOOBfill);
@@ -776,24 +805,36 @@ static Tiled tiled(const void* p, long long ps, int parts, long long bs, long lo
                         q == cudaDriverEntryPointSuccess;
         return ok ? reinterpret_cast<Encode>(f) : nullptr;
     }();
+    if (!enc) return false;
+    cuuint64_t bytes[4];
+    for (int i = 0; i < 4; ++i) {
+        bytes[i] = (cuuint64_t)strides[i] * esz;
+        if (bytes[i] >= (1ull << 40)) return false;
+    }
+    const cuuint32_t box[5] = {(cuuint32_t)(rb / esz), (cuuint32_t)rows, 1, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+    return enc(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5, const_cast<void*>(p), dims.data(),
+               bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A plain [rows][cols] bf16 matrix with boxes of 64 columns x `rows_box` rows.
+static bool encode_map2(CUtensorMap* m, const void* p, int cols, long long rows, int rows_box) {
+    const long long all = rows * cols;
+    return encode_map(m, p, 2, {(cuuint64_t)cols, (cuuint64_t)rows, 1, 1, 1}, {cols, all, all, all}, 128, rows_box);
+}
+
+// The map of a [part][batch][heads][tokens][width] tensor with boxes of 32 tokens x rb bytes.
+static Tiled tiled(const void* p, long long ps, int parts, long long bs, long long hs, long long ts, const Dims& d, int heads, int width,
+                   int esz, int rb) {
     Tiled x{};
     x.p = static_cast<const char*>(p);
     x.ps = ps; x.bs = bs; x.hs = hs; x.ts = ts;
     x.hmul = hs != 0;
     x.bmul = bs != 0;
     // a dimension of size one keeps a stride that is valid
-    const long long row = (long long)width;
-    const cuuint64_t dims[5] = {(cuuint64_t)width, (cuuint64_t)d.N, (cuuint64_t)(hs ? heads : 1), (cuuint64_t)(bs ? d.B : 1),
-                                (cuuint64_t)parts};
-    const cuuint64_t strides[4] = {(cuuint64_t)(ts ? ts : row) * esz, (cuuint64_t)(hs ? hs : row) * esz, (cuuint64_t)(bs ? bs : row) * esz,
-                                   (cuuint64_t)(ps ? ps : row) * esz};
-    const cuuint32_t box[5] = {(cuuint32_t)(rb / esz), CT, 1, 1, 1}, one[5] = {1, 1, 1, 1, 1};
-    bool ok = enc != nullptr && (ts != 0 || d.N == 1);
-    for (cuuint64_t st : strides) ok = ok && st < (1ull << 40);
-    x.tma = ok && enc(&x.map, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5, const_cast<void*>(p), dims,
-                      strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    x.tma = (ts != 0 || d.N == 1) &&
+            encode_map(&x.map, p, esz, {(cuuint64_t)width, (cuuint64_t)d.N, (cuuint64_t)(hs ? heads : 1), (cuuint64_t)(bs ? d.B : 1), (cuuint64_t)parts},
+                       {ts ? ts : width, hs ? hs : width, bs ? bs : width, ps ? ps : width}, rb, CT);
     return x;
 }
 static Tiled tiled(const Parts& x, int parts, const Dims& d, int heads, int width, int rb) {
@@ -821,7 +862,7 @@ static uint32_t* error_word(const Call& c) { return reinterpret_cast<uint32_t*>(
 // Workspace
 // --------------------------------------------------------------------------------------------------
 struct Layout {
-    size_t rec, qp, kp, op, E, Y, S, D, dw, total;
+    size_t rec, qp, kp, op, E, Y, S, D, dw, part, total;
 };
 static Layout layout(const Dims& d, bool fp32, bool backward) {
     const int P = fp32 ? 3 : 2;
@@ -841,6 +882,7 @@ static Layout layout(const Dims& d, bool fp32, bool backward) {
         l.S = take(heads * d.ng * P * d.dv * d.dk * 2);
         l.D = take(heads * d.ng * P * d.dv * d.dk * 2);
         l.dw = take(heads * d.dv * d.dk * 4);
+        if (!fp32 && d.r > 1) l.part = take(2 * toks * d.dk * 4);
     }
     l.total = at;
     return l;
@@ -864,7 +906,7 @@ static Parts as_parts(const View& x, bool fp32, uint8_t* ws, const Dims& d, int 
 
 template <int DK, int P, int PK, bool BACKWARD>
 static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_t* rec) {
-    constexpr int kPrepWarps = prep_warps<DK, PK>(), smem = kPrepWarps * prep_warp_bytes<DK, PK>();
+    constexpr int kPrepWarps = prep_warps<DK, PK>(), smem = kPrepWarps * prep_warp_bytes<DK, P, PK>();
     constexpr auto k = delta_prep<DK, P, PK, BACKWARD>;
     ttt_status st = allow_smem<k>(smem);
     if (st != TTT_OK) return st;
@@ -931,7 +973,7 @@ static ttt_status backward_t(const Call& c) {
     bo.dW0 = reduce ? reinterpret_cast<float*>(c.ws + l.dw) : c.dW0;
     st = run_reverse<DK, P, PK>(c, Q, K, O, rec, bo);
     if (st != TTT_OK) return st;
-    st = run_grads<DK, P, PK>(c, Q, K, O, out, bo);
+    st = run_grads<DK, P, PK>(c, Q, K, O, out, bo, reinterpret_cast<float*>(c.ws + l.part));
     if (st != TTT_OK || !reduce) return st;
     return run_sum_images(bo.dW0, c.dW0, c.d.B, (long long)c.d.h * c.d.dv * DK, c.stream);
 }

@@ -55,6 +55,7 @@ struct Call {
     uint8_t* ws;                      // starts with a header whose first word is the error word
     cudaStream_t stream;
     unsigned long long wait_ns;       // bound of every device-side wait (ns)
+    int sms;                          // SMs of the device
 };
 
 size_t forward_ws_bytes(const Dims& d, bool fp32);

@@ -146,6 +146,13 @@ struct Checker {
     }
 };
 
+// SMs of the current device (148 if it cannot be asked; the launch then reports why).
+static int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    return n;
+}
+
 static ttt_status check_lengths(const int* lengths) {
     if (!lengths) return TTT_OK;
     if (misaligned(lengths, 4)) return TTT_ERR_ALIGNMENT;
@@ -200,6 +207,7 @@ ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const t
     c.W1_out = W1_out;
     c.ws = static_cast<uint8_t*>(ws);
     c.wait_ns = wait_limit_ns();
+    c.sms = sm_count();
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_forward(c);
 }
@@ -247,6 +255,7 @@ ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const 
     c.dW0 = dW0_out;
     c.ws = static_cast<uint8_t*>(ws);
     c.wait_ns = wait_limit_ns();
+    c.sms = sm_count();
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_backward(c);
 }

@@ -701,7 +701,63 @@ static ttt_status run_grads_t(const Call& c, const Parts& Q, const Parts& K, con
                                                                                  fo.S, bo.D, c.dQ, c.dK, c.dG, c.dBeta);
     return check_launch(cudaGetLastError());
 }
+
+#include "delta_grads_tc.cuh"
+
+// A strided bf16 token tensor with boxes of 64 tokens x rb bytes; false where it cannot be mapped.
+static bool map_tokens(CUtensorMap* m, const Parts& x, const Dims& d, int heads, int width, int rb, int* hmul, int* bmul) {
+    *hmul = x.hs != 0;
+    *bmul = x.bs != 0;
+    return encode_map(m, x.p, 2, {(cuuint64_t)width, (cuuint64_t)d.N, (cuuint64_t)(x.hs ? heads : 1), (cuuint64_t)(x.bs ? d.B : 1), 1},
+                      {x.ts ? x.ts : width, x.hs ? x.hs : width, x.bs ? x.bs : width, width}, rb, 64) &&
+           (x.ts != 0 || d.N == 1);
+}
+
+template <int DK>
+static ttt_status run_grads_tc(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo,
+                               float* part, bool* done) {
+    using L = GradsTc<DK>;
+    const Dims& d = c.d;
+    GradsArgs a{};
+    const long long rows = (long long)d.B * d.h * d.N, srows = (long long)d.B * d.h * d.ng * 2 * d.dv;
+    *done = rows < (1LL << 31) - 64 && srows < (1LL << 31) - 64 &&
+            map_tokens(&a.K, K, d, d.hk, DK, 128, &a.kh, &a.kb) && map_tokens(&a.Q, Q, d, d.hk, DK, 128, &a.qh, &a.qb) &&
+            map_tokens(&a.O, O, d, d.h, d.dv, 64, &a.oh, &a.ob) &&
+            encode_map(&a.E, fo.E, 2, {(cuuint64_t)d.dv, (cuuint64_t)rows, 2, 1, 1}, {d.dv, fo.e_ps, fo.e_ps, fo.e_ps}, 64, 64) &&
+            encode_map(&a.Y, bo.Y, 2, {(cuuint64_t)d.dv, (cuuint64_t)rows, 2, 1, 1}, {d.dv, bo.y_ps, bo.y_ps, bo.y_ps}, 64, 64) &&
+            encode_map2(&a.S, fo.S, DK, srows, L::SV) && encode_map2(&a.D, bo.D, DK, srows, L::SV);
+    if (!*done) return TTT_OK;
+    a.d = d;
+    a.G = c.G; a.Beta = c.Beta; a.dG = c.dG; a.dBeta = c.dBeta;
+    a.dQ = c.dQ; a.dK = c.dK;
+    if (d.r > 1) {                             // fp32 sums per value head, then their sum
+        a.out_fp32 = a.out_per_head = 1;
+        a.dQ = View{reinterpret_cast<char*>(part), (long long)d.h * d.N * DK, (long long)d.N * DK, DK};
+        a.dK = View{reinterpret_cast<char*>(part + rows * DK), (long long)d.h * d.N * DK, (long long)d.N * DK, DK};
+    }
+    a.err = error_word(c);
+    a.wait_ns = c.wait_ns;
+    a.items = (long long)d.B * d.h * d.ng;
+    constexpr auto k = delta_grads_tc<DK>;
+    ttt_status st = allow_smem<k>(L::smem);
+    if (st != TTT_OK) return st;
+    k<<<(unsigned)std::min<long long>(a.items, c.sms), 384, L::smem, c.stream>>>(a);
+    st = check_launch(cudaGetLastError());
+    if (st != TTT_OK || d.r == 1) return st;
+    const long long n4 = (long long)d.B * d.hk * d.N * DK / 4;
+    sum_heads<<<(unsigned)((n4 + 255) / 256), 256, 0, c.stream>>>(part, c.dQ, d, n4);
+    sum_heads<<<(unsigned)((n4 + 255) / 256), 256, 0, c.stream>>>(part + rows * DK, c.dK, d, n4);
+    return check_launch(cudaGetLastError());
+}
+
 template <int DK, int P, int PK>
-static ttt_status run_grads(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo) {
+static ttt_status run_grads(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo,
+                            float* part) {
+    if constexpr (PK == 1) {
+        bool done;
+        const ttt_status st = run_grads_tc<DK>(c, Q, K, O, fo, bo, part, &done);
+        if (done) return st;
+    }
+    // fp32 tokens, and token tensors that no tensor map describes (a token stride of zero)
     return c.d.r > 1 ? run_grads_t<DK, P, PK, true>(c, Q, K, O, fo, bo) : run_grads_t<DK, P, PK, false>(c, Q, K, O, fo, bo);
 }

@@ -16,9 +16,11 @@
 namespace ttt {
 namespace clip {
 
-constexpr int kTable = 256;               // tensors per launch
+constexpr int kTable = 256;               // tensors per launch (a small table for up to kSmall: less to pass)
+constexpr int kSmall = 64;
 constexpr int kThreads = 512;
-constexpr int kPiece = kThreads * 16 * 4; // bytes of a tensor that a CTA takes at a time
+constexpr int kLoads = 8;                 // 16-byte loads a thread has in flight
+constexpr int kPiece = kThreads * 16 * kLoads;   // bytes of a tensor that a CTA takes at a time
 constexpr int kMaxCtas = 148 * 4;
 
 struct Item {
@@ -28,12 +30,14 @@ struct Item {
     int first;                            // first piece (over the launch's tensors)
     int fp32;
 };
+template <int M>
 struct Table {
-    Item it[kTable];
+    Item it[M];
     int n, pieces;
 };
 
-__device__ __forceinline__ int find_item(const Table& t, int piece) {
+template <int M>
+__device__ __forceinline__ int find_item(const Table<M>& t, int piece) {
     int lo = 0, hi = t.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -92,22 +96,24 @@ __device__ __forceinline__ double block_sum(double x, double* sm) {
     return x;
 }
 
-__global__ void __launch_bounds__(kThreads) clip_norm(const __grid_constant__ Table t, double* partial) {
+template <int M>
+__global__ void __launch_bounds__(kThreads) clip_norm(const __grid_constant__ Table<M> t, double* partial) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
     __shared__ double sm[kThreads / 32];
     double acc = 0.0;
     for (int piece = blockIdx.x; piece < t.pieces; piece += gridDim.x) {
         const Item& it = t.it[find_item(t, piece)];
         const Range r = range_of(it, piece);
-        uint4 w[4];
-        bool live[4];
+        uint4 w[kLoads];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             const long long o = r.vlo + ((long long)i * kThreads + threadIdx.x) * 16;
-            live[i] = o < r.vhi;
-            w[i] = live[i] ? *reinterpret_cast<const uint4*>(it.in + o) : make_uint4(0, 0, 0, 0);
+            w[i] = o < r.vhi ? *reinterpret_cast<const uint4*>(it.in + o) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc += sq_piece(w[i], it.fp32);
+        for (int i = 0; i < kLoads; ++i)
+            if (w[i].x | w[i].y | w[i].z | w[i].w) acc += sq_piece(w[i], it.fp32);
         const int es = it.fp32 ? 4 : 2, heads = (int)(r.vlo - r.lo) / es, tails = (int)(r.hi - r.vhi) / es;
         if ((int)threadIdx.x < heads + tails) {        // fewer than 16 elements that no vector covers
             const int x = threadIdx.x;
@@ -119,9 +125,11 @@ __global__ void __launch_bounds__(kThreads) clip_norm(const __grid_constant__ Ta
     if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
+template <int M>
 __global__ void __launch_bounds__(kThreads)
-clip_scale(const __grid_constant__ Table t, const double* partial, int n_partial, float max_norm, float* norm_out) {
+clip_scale(const __grid_constant__ Table<M> t, const double* partial, int n_partial, float max_norm, float* norm_out) {
     __shared__ double sm[kThreads / 32];
+    pdl_wait_primary();
     double acc = 0.0;
     for (int i = threadIdx.x; i < n_partial; i += kThreads) acc += partial[i];
     const double norm = sqrt(block_sum(acc, sm));
@@ -134,14 +142,14 @@ clip_scale(const __grid_constant__ Table t, const double* partial, int n_partial
         const Range r = range_of(it, piece);
         const int es = it.fp32 ? 4 : 2;
         const bool vec = ((reinterpret_cast<uintptr_t>(it.in) ^ reinterpret_cast<uintptr_t>(it.out)) & 15) == 0;
-        uint4 w[4];
+        uint4 w[kLoads];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             const long long o = r.vlo + ((long long)i * kThreads + threadIdx.x) * 16;
-            if (o < r.vhi) w[i] = *reinterpret_cast<const uint4*>(it.in + o);
+            if (o < r.vhi) w[i] = __ldcs(reinterpret_cast<const uint4*>(it.in + o));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             const long long o = r.vlo + ((long long)i * kThreads + threadIdx.x) * 16;
             if (o >= r.vhi) continue;
             uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -154,7 +162,7 @@ clip_scale(const __grid_constant__ Table t, const double* partial, int n_partial
             }
             char* out = it.out + o;
             if (vec) {
-                *reinterpret_cast<uint4*>(out) = make_uint4(x[0], x[1], x[2], x[3]);
+                __stcs(reinterpret_cast<uint4*>(out), make_uint4(x[0], x[1], x[2], x[3]));
             } else if (it.fp32) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(out)[j] = x[j];
@@ -188,35 +196,51 @@ size_t clip_ws_bytes(int n) {
     return (size_t)((n + clip::kTable - 1) / clip::kTable) * clip::kMaxCtas * sizeof(double);
 }
 
-ttt_status launch_clip(const void* const* in, void* const* out, const long long* counts, const int* dtypes, int n, float max_norm,
-                       float* norm_out, void* ws, cudaStream_t st) {
+template <int M>
+static ttt_status launch_clip_t(const void* const* in, void* const* out, const long long* counts, const int* dtypes, int n, float max_norm,
+                                float* norm_out, double* partial, cudaStream_t st) {
     using namespace clip;
-    double* partial = static_cast<double*>(ws);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;      // each kernel waits for the one before it
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     int used = 0;
     for (int pass = 0; pass < 2; ++pass)
-        for (int t0 = 0, seg = 0; t0 < n; t0 += kTable, ++seg) {
-            Table t;
+        for (int t0 = 0, seg = 0; t0 < n; t0 += M, ++seg) {
+            Table<M> t;
             t.n = 0;
             t.pieces = 0;
-            for (int i = t0; i < std::min(n, t0 + kTable); ++i) {
+            for (int i = t0; i < std::min(n, t0 + M); ++i) {
                 const int es = dtypes[i] == TTT_FP32 ? 4 : 2;
                 const long long bytes = counts[i] * es;
                 if (bytes == 0) continue;
                 t.it[t.n++] = Item{static_cast<const char*>(in[i]), static_cast<char*>(out[i]), bytes, t.pieces, dtypes[i] == TTT_FP32};
                 t.pieces += pieces_of(in[i], bytes);
             }
+            const int grid = std::max(1, std::min(t.pieces, kMaxCtas));
+            cfg.gridDim = dim3(grid);
+            cudaError_t e;
             if (pass == 0) {
-                const int grid = std::max(1, std::min(t.pieces, kMaxCtas));
-                clip_norm<<<grid, kThreads, 0, st>>>(t, partial + used);
+                e = cudaLaunchKernelEx(&cfg, clip_norm<M>, t, partial + used);
                 used += grid;
             } else {
-                clip_scale<<<std::max(1, std::min(t.pieces, kMaxCtas)), kThreads, 0, st>>>(t, partial, used, max_norm,
-                                                                                           seg == 0 ? norm_out : nullptr);
+                e = cudaLaunchKernelEx(&cfg, clip_scale<M>, t, (const double*)partial, used, max_norm, seg == 0 ? norm_out : (float*)nullptr);
             }
-            const ttt_status s = check_launch(cudaGetLastError());
+            const ttt_status s = check_launch(e);
             if (s != TTT_OK) return s;
         }
     return TTT_OK;
+}
+
+ttt_status launch_clip(const void* const* in, void* const* out, const long long* counts, const int* dtypes, int n, float max_norm,
+                       float* norm_out, void* ws, cudaStream_t st) {
+    double* partial = static_cast<double*>(ws);
+    return n <= clip::kSmall ? launch_clip_t<clip::kSmall>(in, out, counts, dtypes, n, max_norm, norm_out, partial, st)
+                             : launch_clip_t<clip::kTable>(in, out, counts, dtypes, n, max_norm, norm_out, partial, st);
 }
 
 }  // namespace ttt

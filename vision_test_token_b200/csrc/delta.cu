@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <array>
 #include <atomic>
+#include <cstdlib>
 
 #include "delta.cuh"
 
@@ -37,21 +38,30 @@ namespace gd {
 // --------------------------------------------------------------------------------------------------
 // fp32 tokens -> bf16 parts, contiguous [part][B][heads][N][width]
 // --------------------------------------------------------------------------------------------------
+struct SplitArgs {
+    View x[3];
+    __nv_bfloat16* out[3];
+    long long ps[3];                  // elements of a tensor = part stride
+    int heads[3], width[3];
+    int N;
+};
 template <int P>
-__global__ void split_tokens(View x, __nv_bfloat16* out, long long ps, int heads, int N, int width, long long total4) {
-    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total4; i += (long long)gridDim.x * blockDim.x) {
-        const int w4 = width / 4;
-        const int c = (int)(i % w4) * 4;
-        const long long row = i / w4;
-        const int t = (int)(row % N);
-        const long long bh = row / N;
-        const int h = (int)(bh % heads), b = (int)(bh / heads);
-        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x.p) + b * x.bs + h * x.hs + t * x.ts + c);
+__global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ SplitArgs a) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int i = blockIdx.y, w4 = a.width[i] / 4, heads = a.heads[i];
+    const long long total = a.ps[i] / 4;
+    for (long long x = blockIdx.x * 256LL + threadIdx.x; x < total; x += gridDim.x * 256LL) {
+        const int c = (int)(x % w4) * 4;
+        const long long row = x / w4;
+        const int bh = (int)(row / a.N), t = (int)(row - (long long)bh * a.N), b = bh / heads, h = bh - b * heads;
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x[i].p) + b * a.x[i].bs + h * a.x[i].hs +
+                                                          t * a.x[i].ts + c);
         uint32_t lo[P], hi[P];
         split2<P>(v.x, v.y, lo);
         split2<P>(v.z, v.w, hi);
 #pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<uint2*>(out + p * ps + row * width + c) = make_uint2(lo[p], hi[p]);
+        for (int p = 0; p < P; ++p) *reinterpret_cast<uint2*>(a.out[i] + p * a.ps[i] + row * a.width[i] + c) = make_uint2(lo[p], hi[p]);
     }
 }
 
@@ -163,6 +173,8 @@ __global__ void __launch_bounds__(prep_warps<DK, PK>() * 32)
 delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long total, uint32_t* err) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int KP = DK + 8;
+    pdl_launch_dependents();
+    pdl_wait_primary();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long item = (long long)blockIdx.x * prep_warps<DK, PK>() + warp;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0;
@@ -583,17 +595,17 @@ __device__ __forceinline__ float lds1(uint32_t a) {
 // chunk c - 1 from those: its readout (forward), or E and the state to global memory (backward, SAVE);
 // the loading warp is one or two periods ahead.
 template <int DK, int P, int PK, int RT, int KS, bool SAVE>
-__global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
-delta_chain(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ Tiled K, const __grid_constant__ Tiled V, const uint8_t* rec, const float* W0, long long w0_bs, ChainOut out, uint32_t* err,
-            unsigned long long wait_ns) {
+__device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const Tiled& K, const Tiled& V, const uint8_t* rec, const float* W0,
+                                           long long w0_bs, const ChainOut& out, uint32_t* err, unsigned long long wait_ns, int block) {
     using L = ChainLayout<DK, P, PK, RT, KS, SAVE>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
     constexpr int DW = DK / KS, KB = DW / 16, NBW = 4 / KS, CW = RT * KS, HW = RT * kHelp;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int slices = d.dv / L::VW;
-    const int slice = blockIdx.x % slices;
-    const int bh = blockIdx.x / slices, b = bh / d.h, h = bh % d.h;
+    const int slice = block % slices;
+    const int bh = block / slices, b = bh / d.h, h = bh % d.h;
+    pdl_wait_primary();
     const int len = seq_len(d, b), nch = (len + CT - 1) / CT;
     const int v0 = slice * L::VW;
     const long long state = (long long)d.dv * DK;
@@ -791,6 +803,23 @@ delta_chain(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ Til
     if (out.W1) put_state<DK, DW>(s, out.W1 + (long long)bh * state, row0, col0, lane);
 }
 
+struct ChainArgs {
+    Dims d;
+    Tiled Q, K, V;
+    const uint8_t* rec;
+    const float* W0;
+    long long w0_bs;
+    ChainOut out;
+    uint32_t* err;
+    unsigned long long wait_ns;
+};
+template <int DK, int P, int PK, int RT, int KS>
+__global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
+delta_chain(const __grid_constant__ ChainArgs a) {
+    pdl_launch_dependents();
+    chain_body<DK, P, PK, RT, KS, false>(a.d, a.Q, a.K, a.V, a.rec, a.W0, a.w0_bs, a.out, a.err, a.wait_ns, blockIdx.x);
+}
+
 // A five-dimensional tensor map: boxes of `rows` along the second dimension x rb bytes (32, 64 or 128, swizzled alike)
 // along the first.  strides: elements, of dimensions 1 .. 4.
 static bool encode_map(CUtensorMap* m, const void* p, int esz, std::array<cuuint64_t, 5> dims, std::array<long long, 4> strides, int rb,
@@ -841,6 +870,28 @@ static Tiled tiled(const Parts& x, int parts, const Dims& d, int heads, int widt
     return tiled(x.p, x.ps, parts, x.bs, x.hs, x.ts, d, heads, width, 2, rb);
 }
 
+// Launches `k` as a programmatic dependent of what precedes it in the stream: its set-up overlaps that kernel's tail.
+// (Every kernel here waits for its predecessor before it reads or writes global memory.)
+template <class... P, class... A>
+static ttt_status launch(void (*k)(P...), long long grid, int threads, int smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return check_launch(cudaLaunchKernelEx(&cfg, k, P(args)...));
+}
+
+// Shared memory that leaves room for no second CTA of the same kernel on an SM: a grid that fits the SMs is spread over
+// them even while the kernel before it still holds some (two on one SM take longer than two side by side).
+constexpr int kAloneSmem = 116 * 1024;
+static int spread_smem(int smem, long long grid, int sms) { return grid <= sms && smem < kAloneSmem ? kAloneSmem : smem; }
+
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device (set once per kernel and device).
 template <auto kernel>
 static ttt_status allow_smem(int bytes) {
@@ -856,6 +907,7 @@ static ttt_status allow_smem(int bytes) {
 
 static uint32_t* error_word(const Call& c) { return reinterpret_cast<uint32_t*>(c.ws); }
 
+#include "delta_tc.cuh"
 #include "delta_backward.cuh"
 
 // --------------------------------------------------------------------------------------------------
@@ -870,7 +922,8 @@ static Layout layout(const Dims& d, bool fp32, bool backward) {
     size_t at = kWsHeader;
     auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
     const size_t heads = (size_t)d.B * d.h, toks = heads * d.N;
-    l.rec = take(heads * d.nc * rec_bytes(P, backward));
+    const size_t rec = heads * d.nc * rec_bytes(P, backward);
+    l.rec = take(fp32 ? rec : std::max(rec, heads * ((d.N + TC - 1) / TC) * tc_rec_bytes(backward)));
     if (fp32) {
         l.qp = take((size_t)3 * d.B * d.hk * d.N * d.dk * 2);
         l.kp = take((size_t)3 * d.B * d.hk * d.N * d.dk * 2);
@@ -894,15 +947,31 @@ size_t backward_ws_bytes(const Dims& d, bool fp32) { return layout(d, fp32, true
 // Launches
 // --------------------------------------------------------------------------------------------------
 
-// The tokens of x as bf16 parts: x itself (bf16), or 3 parts in the workspace (fp32).
-static Parts as_parts(const View& x, bool fp32, uint8_t* ws, const Dims& d, int heads, int width, cudaStream_t st) {
-    if (!fp32) return Parts{reinterpret_cast<const __nv_bfloat16*>(x.p), 0, x.bs, x.hs, x.ts};
-    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(ws);
-    const long long n = (long long)d.B * heads * d.N * width;
-    const long long blocks = std::min<long long>((n / 4 + 255) / 256, 148 * 16);
-    split_tokens<3><<<(unsigned)blocks, 256, 0, st>>>(x, o, n, heads, d.N, width, n / 4);
-    return Parts{o, n, (long long)heads * d.N * width, (long long)d.N * width, width};
-}
+// Token tensors as bf16 parts: themselves (bf16), or 3 parts each in the workspace (fp32; one launch for all).
+struct Splitter {
+    const Call& c;
+    bool fp32;
+    SplitArgs a{};
+    int n = 0;
+    Parts add(const View& x, uint8_t* ws, int heads, int width) {
+        if (!fp32) return Parts{reinterpret_cast<const __nv_bfloat16*>(x.p), 0, x.bs, x.hs, x.ts};
+        const long long ps = (long long)c.d.B * heads * c.d.N * width;
+        a.x[n] = x;
+        a.out[n] = reinterpret_cast<__nv_bfloat16*>(ws);
+        a.ps[n] = ps;
+        a.heads[n] = heads;
+        a.width[n++] = width;
+        return Parts{reinterpret_cast<__nv_bfloat16*>(ws), ps, (long long)heads * c.d.N * width, (long long)c.d.N * width, width};
+    }
+    ttt_status run() {
+        if (!n) return TTT_OK;
+        a.N = c.d.N;
+        long long most = 0;
+        for (int i = 0; i < n; ++i) most = std::max(most, a.ps[i]);
+        split_tokens<3><<<dim3((unsigned)std::min<long long>((most / 4 + 255) / 256, 148 * 8), n), 256, 0, c.stream>>>(a);
+        return check_launch(cudaGetLastError());
+    }
+};
 
 template <int DK, int P, int PK, bool BACKWARD>
 static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_t* rec) {
@@ -911,59 +980,60 @@ static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_
     ttt_status st = allow_smem<k>(smem);
     if (st != TTT_OK) return st;
     const long long total = (long long)c.d.B * c.d.h * c.d.nc;
-    k<<<(unsigned)((total + kPrepWarps - 1) / kPrepWarps), kPrepWarps * 32, smem, c.stream>>>(c.d, Q, K, c.G, c.Beta, rec, total,
-                                                                                                     error_word(c));
-    return check_launch(cudaGetLastError());
+    return launch(k, (total + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, smem, c.stream, c.d, Q, K, c.G, c.Beta, rec, total, error_word(c));
 }
 
-template <int DK, int P, int PK, int RT, int KS, bool SAVE>
+template <int DK, int P, int PK, int RT, int KS>
 static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
-    using L = ChainLayout<DK, P, PK, RT, KS, SAVE>;
+    using L = ChainLayout<DK, P, PK, RT, KS, false>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a chain CTA");
-    constexpr auto k = delta_chain<DK, P, PK, RT, KS, SAVE>;
-    ttt_status st = allow_smem<k>(L::smem);
+    constexpr auto k = delta_chain<DK, P, PK, RT, KS>;
+    const ttt_status st = allow_smem<k>(std::max(L::smem, kAloneSmem));
     if (st != TTT_OK) return st;
-    const Tiled q = tiled(Q, PK, c.d, c.d.hk, DK, 128), kk = tiled(K, PK, c.d, c.d.hk, DK, 128);
-    const Tiled v = tiled(c.V.p, 0, 1, c.V.bs, c.V.hs, c.V.ts, c.d, c.d.h, c.d.dv, PK == 1 ? 2 : 4, L::VB);
-    k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), seq_warps<RT, KS>() * 32, L::smem, c.stream>>>(c.d, q, kk, v, rec, c.W0, c.w0_bs, out, error_word(c),
-                                                                                                             c.wait_ns);
-    return check_launch(cudaGetLastError());
+    const long long grid = (long long)c.d.B * c.d.h * (c.d.dv / L::VW);
+    const ChainArgs a{c.d, tiled(Q, PK, c.d, c.d.hk, DK, 128), tiled(K, PK, c.d, c.d.hk, DK, 128),
+                      tiled(c.V.p, 0, 1, c.V.bs, c.V.hs, c.V.ts, c.d, c.d.h, c.d.dv, PK == 1 ? 2 : 4, L::VB), rec, c.W0, c.w0_bs, out,
+                      error_word(c), c.wait_ns};
+    return launch(k, grid, seq_warps<RT, KS>() * 32, spread_smem(L::smem, grid, c.sms), c.stream, a);
 }
-template <int DK, int P, int PK, bool SAVE>
-static ttt_status run_chain(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
-    return few_tiles(c.d) ? run_chain_t<DK, P, PK, 1, 2, SAVE>(c, Q, K, rec, out) : run_chain_t<DK, P, PK, 2, 2, SAVE>(c, Q, K, rec, out);
-}
+
+static bool use_tc(const Dims& d) { return !getenv("NOTC"); }
 
 template <int DK, int P, int PK>
 static ttt_status forward_t(const Call& c) {
     const Layout l = layout(c.d, PK == 3, false);
-    const Parts Q = as_parts(c.Q, PK == 3, c.ws + l.qp, c.d, c.d.hk, DK, c.stream);
-    const Parts K = as_parts(c.K, PK == 3, c.ws + l.kp, c.d, c.d.hk, DK, c.stream);
-    ttt_status st = run_prep<DK, P, PK, false>(c, Q, K, c.ws + l.rec);
+    if constexpr (PK == 1) {
+        TcArgs a{};
+        if (use_tc(c.d) && tc_args(&a, c, false, c.ws + l.rec)) {
+            a.W0 = c.W0;
+            a.w0_bs = c.w0_bs;
+            a.W1 = c.W1_out;
+            a.Z = c.Z;
+            const ttt_status st = run_prep64<DK, false>(c, c.ws + l.rec);
+            return st != TTT_OK ? st : chain_tc<DK, false>(c, a);
+        }
+    }
+    Splitter split{c, PK == 3};
+    const Parts Q = split.add(c.Q, c.ws + l.qp, c.d.hk, DK), K = split.add(c.K, c.ws + l.kp, c.d.hk, DK);
+    ttt_status st = split.run();
+    if (st == TTT_OK) st = run_prep<DK, P, PK, false>(c, Q, K, c.ws + l.rec);
     if (st != TTT_OK) return st;
     ChainOut out{};
     out.Z = c.Z;
     out.W1 = c.W1_out;
-    return run_chain<DK, P, PK, false>(c, Q, K, c.ws + l.rec, out);
+    return few_tiles(c.d) ? run_chain_t<DK, P, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
 }
 
 template <int DK, int P, int PK>
 static ttt_status backward_t(const Call& c) {
     constexpr bool F = PK == 3;
     const Layout l = layout(c.d, F, true);
-    const Parts Q = as_parts(c.Q, F, c.ws + l.qp, c.d, c.d.hk, DK, c.stream);
-    const Parts K = as_parts(c.K, F, c.ws + l.kp, c.d, c.d.hk, DK, c.stream);
-    const Parts O = as_parts(c.Z, F, c.ws + l.op, c.d, c.d.h, c.d.dv, c.stream);
     uint8_t* rec = c.ws + l.rec;
-    ttt_status st = run_prep<DK, P, PK, true>(c, Q, K, rec);
-    if (st != TTT_OK) return st;
     const long long ps = (long long)c.d.B * c.d.h * c.d.N * c.d.dv;
     ChainOut out{};
     out.E = reinterpret_cast<__nv_bfloat16*>(c.ws + l.E);
     out.e_ps = ps;
     out.S = reinterpret_cast<__nv_bfloat16*>(c.ws + l.S);
-    st = run_chain<DK, P, PK, true>(c, Q, K, rec, out);
-    if (st != TTT_OK) return st;
     BackOut bo{};
     bo.dV = c.dV;
     bo.Y = reinterpret_cast<__nv_bfloat16*>(c.ws + l.Y);
@@ -971,9 +1041,40 @@ static ttt_status backward_t(const Call& c) {
     bo.D = reinterpret_cast<__nv_bfloat16*>(c.ws + l.D);
     const bool reduce = c.dW0 && c.w0_bs == 0;
     bo.dW0 = reduce ? reinterpret_cast<float*>(c.ws + l.dw) : c.dW0;
-    st = run_reverse<DK, P, PK>(c, Q, K, O, rec, bo);
+    Splitter split{c, F};
+    const Parts Q = split.add(c.Q, c.ws + l.qp, c.d.hk, DK), K = split.add(c.K, c.ws + l.kp, c.d.hk, DK),
+                O = split.add(c.Z, c.ws + l.op, c.d.h, c.d.dv);
+    ttt_status st = split.run();
     if (st != TTT_OK) return st;
-    st = run_grads<DK, P, PK>(c, Q, K, O, out, bo, reinterpret_cast<float*>(c.ws + l.part));
+    bool done = false;
+    if constexpr (PK == 1) {
+        TcArgs a{}, r{};
+        if (use_tc(c.d) && tc_args(&a, c, true, rec) && map64(&r.V, O, c.d, c.d.h, c.d.dv)) {
+            a.W0 = c.W0;
+            a.w0_bs = c.w0_bs;
+            a.E = out.E;
+            a.S = out.S;
+            a.e_ps = ps;
+            const Tok64 o = r.V;
+            r = a;
+            r.V = o;
+            r.W0 = c.dW1;
+            r.w0_bs = (long long)c.d.h * c.d.dv * DK;
+            r.W1 = bo.dW0;
+            r.Z = c.dV;
+            r.E = bo.Y;
+            r.S = bo.D;
+            st = run_prep64<DK, true>(c, rec);
+            if (st == TTT_OK) st = chain_tc<DK, true>(c, a);
+            if (st == TTT_OK) st = c.d.dv == 64 ? run_reverse_tc<DK, 64>(c, r) : run_reverse_tc<DK, 128>(c, r);
+            done = true;
+        }
+    }
+    if (!done) {
+        st = run_prep<DK, P, PK, true>(c, Q, K, rec);
+        if (st == TTT_OK) st = run_both<DK, P, PK>(c, Q, K, O, rec, out, bo);
+    }
+    if (st == TTT_OK) st = run_grads<DK, P, PK>(c, Q, K, O, out, bo, reinterpret_cast<float*>(c.ws + l.part));
     if (st != TTT_OK || !reduce) return st;
     return run_sum_images(bo.dW0, c.dW0, c.d.B, (long long)c.d.h * c.d.dv * DK, c.stream);
 }

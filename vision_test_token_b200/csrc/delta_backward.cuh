@@ -46,17 +46,17 @@ struct ReverseLayout {
 // prepare what chunk k + 1 needs of dZ alone (A^T dZ, and scale gamma dZ as operand parts) and write what chunk
 // k - 1 gave (Y, dV, and the adjoint it started from).
 template <int DK, int P, int PK, int RT, int KS>
-__global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
-delta_reverse(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ Tiled K, const __grid_constant__ Tiled O, const uint8_t* rec, const float* dW1, BackOut out, uint32_t* err,
-              unsigned long long wait_ns) {
+__device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, const Tiled& K, const Tiled& O, const uint8_t* rec, const float* dW1,
+                                             const BackOut& out, uint32_t* err, unsigned long long wait_ns, int block) {
     using L = ReverseLayout<DK, P, PK, RT, KS>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
     constexpr int DW = DK / KS, KB = DW / 16, NBW = 4 / KS, CW = RT * KS, HW = RT * kHelp;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3;
     const int slices = d.dv / L::VW;
-    const int slice = blockIdx.x % slices;
-    const int bh = blockIdx.x / slices, b = bh / d.h, h = bh % d.h;
+    const int slice = block % slices;
+    const int bh = block / slices, b = bh / d.h, h = bh % d.h;
+    pdl_wait_primary();
     const int len = seq_len(d, b), nch = (len + CT - 1) / CT;
     const int v0 = slice * L::VW;
     const long long state = (long long)d.dv * DK;
@@ -261,6 +261,29 @@ delta_reverse(Dims d, const __grid_constant__ Tiled Q, const __grid_constant__ T
     if (out.dW0) put_state<DK, DW>(s, out.dW0 + bh * state, row0, col0, lane);
 }
 
+// The backward pass's two sequential kernels need only the prep kernel: one launch runs both, the longer one first.
+struct BothArgs {
+    Dims d;
+    Tiled Q, K, V, O;
+    const uint8_t* rec;
+    const float *W0, *dW1;
+    long long w0_bs;
+    ChainOut chain;
+    BackOut back;
+    uint32_t* err;
+    unsigned long long wait_ns;
+    int half;                     // CTAs of each
+};
+template <int DK, int P, int PK, int RT, int KS>
+__global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
+delta_both(const __grid_constant__ BothArgs a) {
+    pdl_launch_dependents();
+    if ((int)blockIdx.x < a.half)
+        reverse_body<DK, P, PK, RT, KS>(a.d, a.Q, a.K, a.O, a.rec, a.dW1, a.back, a.err, a.wait_ns, blockIdx.x);
+    else
+        chain_body<DK, P, PK, RT, KS, true>(a.d, a.Q, a.K, a.V, a.rec, a.W0, a.w0_bs, a.chain, a.err, a.wait_ns, blockIdx.x - a.half);
+}
+
 // --------------------------------------------------------------------------------------------------
 // Token gradients
 // --------------------------------------------------------------------------------------------------
@@ -291,6 +314,8 @@ delta_grads(Dims d, Parts Q, Parts K, Parts O, View G, View Beta, const __nv_bfl
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int mi = lane >> 3, lr = lane & 7;
     const int wm = warp % WM, wn = warp / WM;
+    pdl_launch_dependents();
+    pdl_wait_primary();
     const int grp = blockIdx.x % d.ng;
     const int bk = blockIdx.x / d.ng, b = bk / d.hk, kh = bk % d.hk;
     const int left = min(GT, seq_len(d, b) - grp * GT);
@@ -659,6 +684,7 @@ delta_grads(Dims d, Parts Q, Parts K, Parts O, View G, View Beta, const __nv_bfl
 
 // out = the sum over images of [B][n], in image order.
 static __global__ void sum_images(const float* part, float* out, int B, long long n) {
+    pdl_wait_primary();
     const long long x = blockIdx.x * (long long)blockDim.x + threadIdx.x;
     if (x >= n) return;
     float a = 0.f;
@@ -667,27 +693,31 @@ static __global__ void sum_images(const float* part, float* out, int B, long lon
 }
 
 static ttt_status run_sum_images(const float* part, float* out, int B, long long n, cudaStream_t st) {
-    sum_images<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, out, B, n);
-    return check_launch(cudaGetLastError());
+    return launch(sum_images, (n + 255) / 256, 256, 0, st, part, out, B, n);
 }
 
 template <int DK, int P, int PK, int RT, int KS>
-static ttt_status run_reverse_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const BackOut& out) {
-    using L = ReverseLayout<DK, P, PK, RT, KS>;
-    static_assert(L::smem <= 227 * 1024, "shared memory of a reverse CTA");
-    constexpr auto k = delta_reverse<DK, P, PK, RT, KS>;
-    ttt_status st = allow_smem<k>(L::smem);
+static ttt_status run_both_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const ChainOut& out,
+                             const BackOut& bo) {
+    using R = ReverseLayout<DK, P, PK, RT, KS>;
+    using F = ChainLayout<DK, P, PK, RT, KS, true>;
+    constexpr int smem = R::smem > F::smem ? R::smem : F::smem;
+    static_assert(smem <= 227 * 1024, "shared memory of a sequential CTA");
+    constexpr auto k = delta_both<DK, P, PK, RT, KS>;
+    const ttt_status st = allow_smem<k>(std::max(smem, kAloneSmem));
     if (st != TTT_OK) return st;
-    const Tiled q = tiled(Q, PK, c.d, c.d.hk, DK, 128), kk = tiled(K, PK, c.d, c.d.hk, DK, 128), o = tiled(O, PK, c.d, c.d.h, c.d.dv, L::VB);
-    k<<<(unsigned)(c.d.B * c.d.h * (c.d.dv / L::VW)), seq_warps<RT, KS>() * 32, L::smem, c.stream>>>(c.d, q, kk, o, rec, c.dW1, out, error_word(c),
-                                                                                                             c.wait_ns);
-    return check_launch(cudaGetLastError());
+    const int half = c.d.B * c.d.h * (c.d.dv / (RT * 16));
+    const BothArgs a{c.d, tiled(Q, PK, c.d, c.d.hk, DK, 128), tiled(K, PK, c.d, c.d.hk, DK, 128),
+                     tiled(c.V.p, 0, 1, c.V.bs, c.V.hs, c.V.ts, c.d, c.d.h, c.d.dv, PK == 1 ? 2 : 4, F::VB),
+                     tiled(O, PK, c.d, c.d.h, c.d.dv, R::VB), rec, c.W0, c.dW1, c.w0_bs, out, bo, error_word(c), c.wait_ns, half};
+    return launch(k, 2LL * half, seq_warps<RT, KS>() * 32, spread_smem(smem, 2LL * half, c.sms), c.stream, a);
 }
 template <int DK, int P, int PK>
-static ttt_status run_reverse(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const BackOut& out) {
+static ttt_status run_both(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const ChainOut& out,
+                           const BackOut& bo) {
     // fp32: the three parts of a second tile do not fit the shared memory
-    if (PK == 3 || few_tiles(c.d)) return run_reverse_t<DK, P, PK, 1, 2>(c, Q, K, O, rec, out);
-    return run_reverse_t<DK, P, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out);
+    if (PK == 3 || few_tiles(c.d)) return run_both_t<DK, P, PK, 1, 2>(c, Q, K, O, rec, out, bo);
+    return run_both_t<DK, P, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out, bo);
 }
 
 template <int DK, int P, int PK, bool GROUP>
@@ -697,9 +727,8 @@ static ttt_status run_grads_t(const Call& c, const Parts& Q, const Parts& K, con
     constexpr auto k = delta_grads<DK, P, PK, GROUP>;
     ttt_status st = allow_smem<k>(L::smem);
     if (st != TTT_OK) return st;
-    k<<<(unsigned)((long long)c.d.B * c.d.hk * c.d.ng), 256, L::smem, c.stream>>>(c.d, Q, K, O, c.G, c.Beta, fo.E, bo.Y, fo.e_ps,
-                                                                                 fo.S, bo.D, c.dQ, c.dK, c.dG, c.dBeta);
-    return check_launch(cudaGetLastError());
+    return launch(k, (long long)c.d.B * c.d.hk * c.d.ng, 256, L::smem, c.stream, c.d, Q, K, O, c.G, c.Beta, fo.E, bo.Y, fo.e_ps, fo.S, bo.D, c.dQ,
+                  c.dK, c.dG, c.dBeta);
 }
 
 #include "delta_grads_tc.cuh"
@@ -741,13 +770,10 @@ static ttt_status run_grads_tc(const Call& c, const Parts& Q, const Parts& K, co
     constexpr auto k = delta_grads_tc<DK>;
     ttt_status st = allow_smem<k>(L::smem);
     if (st != TTT_OK) return st;
-    k<<<(unsigned)std::min<long long>(a.items, c.sms), 384, L::smem, c.stream>>>(a);
-    st = check_launch(cudaGetLastError());
+    st = launch(k, std::min<long long>(a.items, c.sms), 384, L::smem, c.stream, a);
     if (st != TTT_OK || d.r == 1) return st;
     const long long n4 = (long long)d.B * d.hk * d.N * DK / 4;
-    sum_heads<<<(unsigned)((n4 + 255) / 256), 256, 0, c.stream>>>(part, c.dQ, d, n4);
-    sum_heads<<<(unsigned)((n4 + 255) / 256), 256, 0, c.stream>>>(part + rows * DK, c.dK, d, n4);
-    return check_launch(cudaGetLastError());
+    return launch(sum_heads, 2 * ((n4 + 255) / 256), 256, 0, c.stream, part, part + rows * DK, c.dQ, c.dK, d, n4);
 }
 
 template <int DK, int P, int PK>

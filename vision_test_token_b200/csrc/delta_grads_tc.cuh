@@ -59,27 +59,6 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(512 >> 4) << 32) | (1ull << 46) |
            (4ull << 61);
 }
-__device__ __forceinline__ void tma_load_5d_at(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2, int c3, int c4) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(m), "r"(s32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-        : "memory");
-}
-// One thread of a converged warp.  Products issued inside `if (elect_one())` from warp-uniform descriptors take the
-// tensor core's own time (35 cycles for 128 x 64 x 16); behind `lane == 0` the compiler moves every operand
-// to a uniform register first (about 50).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
-    return e != 0;
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t col, float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 16) tmem_ld16(col + i, *reinterpret_cast<float(*)[16]>(&v[i]));
-    tmem_ld_wait();
-}
-
 template <int DK>
 __global__ void __launch_bounds__(384, 1)
 delta_grads_tc(const __grid_constant__ GradsArgs p) {
@@ -128,6 +107,8 @@ delta_grads_tc(const __grid_constant__ GradsArgs p) {
         tmem_alloc(&ctl.tmem, 512);
         tmem_relinquish();
     }
+    pdl_launch_dependents();
+    pdl_wait_primary();
     __syncthreads();
     tc_fence_before();
     __syncthreads();
@@ -563,10 +544,15 @@ delta_grads_tc(const __grid_constant__ GradsArgs p) {
     if (warp == 9) tmem_dealloc(ctl.tmem, 512);
 }
 
-// out [B][hk][N][dk] (a strided view) = the sum over the r value heads of a key head of part [B][h][N][dk], in head order.
-static __global__ void sum_heads(const float* part, View out, Dims d, long long n4) {
-    const long long x = blockIdx.x * (long long)blockDim.x + threadIdx.x;
+// dQ, dK [B][hk][N][dk] (strided views; half of the grid each) = the sums over the r value heads of a key head of the fp32
+// [B][h][N][dk] partial gradients, in head order.
+static __global__ void __launch_bounds__(256) sum_heads(const float* pq, const float* pk, View dQ, View dK, Dims d, long long n4) {
+    pdl_wait_primary();
+    const bool second = blockIdx.x >= gridDim.x / 2;
+    const long long x = (blockIdx.x - (second ? gridDim.x / 2 : 0)) * 256LL + threadIdx.x;
     if (x >= n4) return;
+    const float* part = second ? pk : pq;
+    const View& out = second ? dK : dQ;
     const int w4 = d.dk / 4, c = (int)(x % w4) * 4;
     const long long row = x / w4;
     const int t = (int)(row % d.N), kh = (int)(row / d.N % d.hk), b = (int)(row / d.N / d.hk);

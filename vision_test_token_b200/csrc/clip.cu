@@ -18,10 +18,10 @@ namespace clip {
 
 constexpr int kTable = 256;               // tensors per launch (a small table for up to kSmall: less to pass)
 constexpr int kSmall = 64;
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kLoads = 8;                 // 16-byte loads a thread has in flight
 constexpr int kPiece = kThreads * 16 * kLoads;   // bytes of a tensor that a CTA takes at a time
-constexpr int kMaxCtas = 148 * 4;
+constexpr int kMaxCtas = 148 * 32;         // several waves: 377 us with as many CTAs as fit at a time, 341 us with these (667 MB of gradients)
 
 struct Item {
     const char* in;

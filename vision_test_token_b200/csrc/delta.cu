@@ -997,20 +997,19 @@ static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, con
     return launch(k, grid, seq_warps<RT, KS>() * 32, spread_smem(L::smem, grid, c.sms), c.stream, a);
 }
 
-static bool use_tc(const Dims& d) { return !getenv("NOTC"); }
+static bool use_tc(const Dims& d) { return d.dv == MV && !getenv("NOTC"); }
 
 template <int DK, int P, int PK>
 static ttt_status forward_t(const Call& c) {
     const Layout l = layout(c.d, PK == 3, false);
     if constexpr (PK == 1) {
         TcArgs a{};
-        if (use_tc(c.d) && tc_args(&a, c, false, c.ws + l.rec)) {
+        if (use_tc(c.d) && tc_args(&a, c, false, c.ws + l.rec) && tc_outputs(&a, c.Z, c.d, nullptr, 0, nullptr)) {
             a.W0 = c.W0;
             a.w0_bs = c.w0_bs;
             a.W1 = c.W1_out;
-            a.Z = c.Z;
             const ttt_status st = run_prep64<DK, false>(c, c.ws + l.rec);
-            return st != TTT_OK ? st : chain_tc<DK, false>(c, a);
+            return st != TTT_OK ? st : run_chain_tc<DK>(c, a);
         }
     }
     Splitter split{c, PK == 3};
@@ -1048,25 +1047,18 @@ static ttt_status backward_t(const Call& c) {
     if (st != TTT_OK) return st;
     bool done = false;
     if constexpr (PK == 1) {
-        TcArgs a{}, r{};
-        if (use_tc(c.d) && tc_args(&a, c, true, rec) && map64(&r.V, O, c.d, c.d.h, c.d.dv)) {
+        TcArgs a{};
+        bool ok = use_tc(c.d) && tc_args(&a, c, true, rec);
+        TcArgs r = a;
+        ok = ok && map64(&r.V, O, c.d, c.d.h, c.d.dv) && tc_outputs(&a, c.dV, c.d, out.E, ps, out.S) && tc_outputs(&r, c.dV, c.d, bo.Y, ps, bo.D);
+        if (ok) {
             a.W0 = c.W0;
             a.w0_bs = c.w0_bs;
-            a.E = out.E;
-            a.S = out.S;
-            a.e_ps = ps;
-            const Tok64 o = r.V;
-            r = a;
-            r.V = o;
             r.W0 = c.dW1;
             r.w0_bs = (long long)c.d.h * c.d.dv * DK;
             r.W1 = bo.dW0;
-            r.Z = c.dV;
-            r.E = bo.Y;
-            r.S = bo.D;
             st = run_prep64<DK, true>(c, rec);
-            if (st == TTT_OK) st = chain_tc<DK, true>(c, a);
-            if (st == TTT_OK) st = c.d.dv == 64 ? run_reverse_tc<DK, 64>(c, r) : run_reverse_tc<DK, 128>(c, r);
+            if (st == TTT_OK) st = run_both_tc<DK>(c, a, r);
             done = true;
         }
     }

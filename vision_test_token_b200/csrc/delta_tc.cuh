@@ -15,6 +15,7 @@
 // four elementwise passes over [d_v x 64 .. d_k] values by eight warps.
 
 constexpr int TC = 64;                        // tokens per chunk
+constexpr int MV = 128;                       // rows of the state, d_v: the lanes of tensor memory
 constexpr int kTcGates = 1024;                // gamma, suffix, beta (3 x 64 fp32), padded
 constexpr int kTcMat = 2 * TC * 128;          // two parts of a 64 x 64 bf16 matrix, rows of 128 swizzled bytes
 __host__ __device__ constexpr int tc_rec_bytes(bool backward) { return kTcGates + (backward ? 3 : 2) * kTcMat; }
@@ -61,8 +62,7 @@ struct Prep64 {
     static constexpr int blocks = (BACKWARD ? 6 : 3) * CT * BP2 * 4;               // diagonal inverses and a product, per inverse
     static constexpr int extra = blocks > TC * GP2 * 4 ? blocks - TC * GP2 * 4 : 0;   // what Q K^T's place does not hold
     static constexpr int oImg = (front + extra + 127) / 128 * 128;
-    static constexpr int nImg = BACKWARD ? 3 : 2;
-    static constexpr int oRow = oImg + nImg * kTcMat;          // g, beta, suffix inside 32
+    static constexpr int oRow = oImg + kTcMat;                 // one image at a time; g, beta, suffix inside 32
     static constexpr int smem = oRow + 3 * TC * 4;
 };
 
@@ -94,15 +94,20 @@ __device__ __forceinline__ void solve32(const float* g, float left, float right,
         y[i] = x * __shfl_sync(~0u, right, i);
     }
 }
-// Rows 8 w .. 8 w + 7, column `lane` of A B (32 x 32 each); A's columns scaled by `right` (lane l holds column l's).
-__device__ __forceinline__ void mul32(float (&c)[8], const float* a, int pitch, float right, const float* b, int w, int lane) {
+// Rows 8 w .. 8 w + 7, column `lane` of A B, or of A diag(right) B (32 x 32 each).
+template <bool SCALE>
+__device__ __forceinline__ void mul32(float (&c)[8], const float* a, int pitch, const float* right, const float* b, int w, int lane) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) c[r] = 0.f;
 #pragma unroll
     for (int l = 0; l < CT; l += 4) {
         float x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = b[(l + k) * BP2 + lane] * __shfl_sync(~0u, right, l + k);
+        for (int k = 0; k < 4; ++k) x[k] = b[(l + k) * BP2 + lane];
+        if (SCALE) {
+            const float4 s = *reinterpret_cast<const float4*>(right + l);
+            x[0] *= s.x; x[1] *= s.y; x[2] *= s.z; x[3] *= s.w;
+        }
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const float4 v = *reinterpret_cast<const float4*>(a + (w * 8 + r) * pitch + l);
@@ -171,7 +176,12 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
         gates[TC + t] = expf(warp ? suf : suf + other);
         gates[2 * TC + t] = beta;
     }
-    for (int x = tid; x < L::nImg * kTcMat / 16; x += 128) reinterpret_cast<uint4*>(img)[x] = make_uint4(0, 0, 0, 0);
+    for (int x = tid; x < kTcMat / 16; x += 128) reinterpret_cast<uint4*>(img)[x] = make_uint4(0, 0, 0, 0);   // what lies above the diagonal
+    auto copy_out = [&](int m) {
+#pragma unroll
+        for (int x = 0; x < kTcMat / 16; x += 128)
+            reinterpret_cast<uint4*>(out + kTcGates + m * kTcMat)[x + tid] = reinterpret_cast<const uint4*>(img)[x + tid];
+    };
     cp_wait<0>();
     __syncthreads();
     {
@@ -225,11 +235,12 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
         for (int i = i0; i < i0 + n; ++i) {
             if (i > j) s += gr[i];
             const float dec = i >= j ? __expf(s) : 0.f;        // relative error about 2^-22 (1 + |s|)
-            if (i >= j) put_img(img + kTcMat, i, j, d.scale * dec * qkm[i * GP2 + j]);
+            if (i >= j) put_img(img, i, j, d.scale * dec * qkm[i * GP2 + j]);
             kkm[i * GP2 + j] = i > j ? dec * kkm[i * GP2 + j] : 0.f;
         }
     }
     __syncthreads();
+    copy_out(1);                                               // A
     const int nb = CT * BP2;
     const float b0 = br[lane], b1 = br[32 + lane];
     // diagonal blocks: T' = (I + G beta)^{-1} (warps 0, 1), T_u = (I + beta G)^{-1} (warps 2, 3)
@@ -240,35 +251,31 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
     __syncthreads();
     // the block below: - T'_22 (G_21 beta_1 T'_11), and - T_u22 (beta_2 G_21 T_u11)
     float p[8], u[8];
-    mul32(p, kkm + 32 * GP2, GP2, b0, blk, warp, lane);
-    if (BACKWARD) mul32(u, kkm + 32 * GP2, GP2, 1.f, blk + 3 * nb, warp, lane);
+    mul32<true>(p, kkm + 32 * GP2, GP2, br, blk, warp, lane);
+    if (BACKWARD) mul32<false>(u, kkm + 32 * GP2, GP2, br, blk + 3 * nb, warp, lane);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
         blk[2 * nb + (warp * 8 + r) * BP2 + lane] = p[r];
         if (BACKWARD) blk[5 * nb + (warp * 8 + r) * BP2 + lane] = br[32 + warp * 8 + r] * u[r];
     }
     __syncthreads();
-    mul32(p, blk + nb, BP2, 1.f, blk + 2 * nb, warp, lane);
-    if (BACKWARD) mul32(u, blk + 4 * nb, BP2, 1.f, blk + 5 * nb, warp, lane);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const int i = warp * 8 + r;
-        put_img(img, 32 + i, lane, -p[r]);
-        if (lane <= i) {
-            put_img(img, i, lane, blk[i * BP2 + lane]);
-            put_img(img, 32 + i, 32 + lane, blk[nb + i * BP2 + lane]);
-        }
-        if (BACKWARD) {
-            put_img(img + 2 * kTcMat, 32 + i, lane, -u[r]);
+    for (int m = 0; m < (BACKWARD ? 2 : 1); ++m) {
+        const float* q = blk + 3 * nb * m;
+        mul32<false>(p, q + nb, BP2, br, q + 2 * nb, warp, lane);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int i = warp * 8 + r;
+            put_img(img, 32 + i, lane, -p[r]);
             if (lane <= i) {
-                put_img(img + 2 * kTcMat, i, lane, blk[3 * nb + i * BP2 + lane]);
-                put_img(img + 2 * kTcMat, 32 + i, 32 + lane, blk[4 * nb + i * BP2 + lane]);
+                put_img(img, i, lane, q[i * BP2 + lane]);
+                put_img(img, 32 + i, 32 + lane, q[nb + i * BP2 + lane]);
             }
         }
+        __syncthreads();
+        copy_out(2 * m);
+        if (BACKWARD && m == 0) __syncthreads();
     }
-    __syncthreads();
-    for (int x = tid; x < L::nImg * kTcMat / 16; x += 128)
-        reinterpret_cast<uint4*>(out + kTcGates)[x] = reinterpret_cast<const uint4*>(img)[x];
 }
 
 // --------------------------------------------------------------------------------------------------
@@ -317,24 +324,41 @@ struct TcArgs {
     long long w0_bs;
     float* W1;                         // nullable: last state, or the gradient of the first, [B][h][dv][dk]
     View Z;                            // forward: the readout; reverse: dV
-    __nv_bfloat16 *E, *S;              // E (or Y) [2][B][h][N][dv], states (or adjoints) at the chunks' starts (ends) [B][h][ng][2][dv][dk]
-    long long e_ps;
+    CUtensorMap mZ, mE, mS;            // Z; E (or Y) [2][B][h][N][dv]; states (adjoints) at the chunks' starts (ends) [B][h][ng][2][dv][dk]
+    int zh, zb;                        // 0 where Z has one head or image
     uint32_t* err;
     unsigned long long wait_ns;
 };
 
 struct TcCtl {
-    uint64_t full[3], empty[3], sp, xd, rp, ed, up, sd, z1, z1free, z2, z2free, spfree, fr;
+    uint64_t full[3], empty[3], sp, xd, rp, ed, up, sd, z1, z1free, z2, z2free, spfree, fr, spa, ur;
     uint32_t tmem;
     int abort_flag;
 };
 
-template <int DK, int MV, bool SAVE>
+// acc [. x 64 tokens] = (the state's parts) X^T, X a token tile, issued by one thread of the calling warp.  d_k = 128: in
+// two halves, the first 32 columns of each warp half's 64, then the others, as the chain warps write them.
+template <int DK>
+__device__ __forceinline__ void state_product(uint32_t acc, uint32_t parts, uint32_t x, uint32_t id, int half) {
+    if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int kk = DK == 128 ? (i / 2) * 4 + half * 2 + i % 2 : i;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+                mma_bf16_ts(acc, parts + part * (DK / 2) + kk * 8, sdesc_sw128(x + (kk / 4) * TC * 128 + (kk % 4) * 32, 16, 1024), id,
+                            half > 0 || i > 0 || part > 0);
+        }
+    }
+    __syncwarp();
+}
+
+template <int DK, bool SAVE>
 struct TcChain {
     static constexpr int oT = kTcGates, oA = oT + kTcMat, oK = oA + (SAVE ? 0 : kTcMat), oQ = oK + DK * 128, oV = oQ + (SAVE ? 0 : DK * 128);
     static constexpr int stage = oV + MV * 128;
-    static constexpr int kStages = SAVE ? 3 : 2;
-    static constexpr int used = kStages * stage + 512 + 1024, smem = used > 116 * 1024 ? used : 116 * 1024;   // one CTA per SM
+    static constexpr int kStages = SAVE ? 3 : 2, kSlots = SAVE ? 3 : 2;
+    static constexpr int used = kStages * stage + kSlots * MV * 128 + 512 + 1024, smem = used > 116 * 1024 ? used : 116 * 1024;   // one CTA per SM
     static_assert(smem <= 227 * 1024 && stage % 1024 == 0, "shared memory of a chain CTA");
     // tensor-memory columns: state, its parts (hi, lo), X / E / A U, R then U parts, suffix U parts, Q W^T
     static constexpr uint32_t cS = 0, cP = DK, cX = 2 * DK, cR = cX + 64, cU = cR + 64, cZ = cU + 64;
@@ -345,10 +369,9 @@ __device__ __forceinline__ void tmem_st_parts(uint32_t hi, uint32_t lo, const fl
     uint32_t h[16], l[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        uint32_t o[2];
-        split2<2>(v[2 * i], v[2 * i + 1], o);
-        h[i] = o[0];
-        l[i] = o[1];
+        h[i] = pack2(v[2 * i], v[2 * i + 1]);
+        const float2 rest = ffma2(make_float2(lo_f(h[i]), hi_f(h[i])), make_float2(-1.f, -1.f), make_float2(v[2 * i], v[2 * i + 1]));
+        l[i] = pack2(rest.x, rest.y);
     }
     tmem_st16(hi, h);
     tmem_st16(lo, l);
@@ -359,29 +382,77 @@ __device__ __forceinline__ void tc_arrive(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
 }
-// Part p (of two) of a [tokens][dv] matrix: 32 tokens' values of this thread's row, two bytes each (a warp's rows are
-// consecutive features).
-__device__ __forceinline__ void put_column(__nv_bfloat16* dst, long long ts, const float (&v)[32], int left, bool active) {
-    if (!active) return;
+// The four output warps' way to global memory: tiles are laid out in a ring of shared-memory slots as TMA reads
+// them (rows of 128 bytes, swizzled) and stored by it; one thread issues the stores.
+template <int SLOTS>
+struct OutRing {
+    static constexpr int kSlot = MV * 128;
+    uint32_t base;
+    int lane;
+    bool issuer;
+    int job;
+    __device__ __forceinline__ uint32_t open() {       // a slot that no store still reads
+        if (issuer) bulk_wait_read<SLOTS - 1>();
+        named_bar_sync(3, 128);
+        return base + (job++ % SLOTS) * kSlot;
+    }
+    __device__ __forceinline__ void ready() {
+        fence_proxy_async_smem();
+        named_bar_sync(3, 128);
+    }
+    __device__ __forceinline__ void store(const CUtensorMap* m, uint32_t slot, int c0, int c1, int c2, int c3) {
+        asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, 0}], [%1];" ::"l"(m), "r"(slot), "r"(c0),
+                     "r"(c1), "r"(c2), "r"(c3)
+                     : "memory");
+    }
+    // this thread's row of a [MV][64] tile: 32 packed pairs
+    __device__ __forceinline__ void put_row(uint32_t slot, int row, const float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < left) {
-            const uint32_t w = pack2(v[i], 0.f);
-            reinterpret_cast<uint16_t*>(dst)[i * ts] = (uint16_t)w;
+        for (int k = 0; k < 8; ++k)
+            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(slot + row * 128 + ((k ^ (row & 7)) << 4)), "f"(v[4 * k]), "f"(v[4 * k + 1]),
+                         "f"(v[4 * k + 2]), "f"(v[4 * k + 3])
+                         : "memory");
+    }
+    // this thread's feature of 32 tokens from t0 on of a [MV / 64][64 tokens][64] tile, rounded to bf16
+    __device__ __forceinline__ void put_column(uint32_t slot, int row, int t0, const float (&v)[32]) {
+        const uint32_t at = slot + (row >> 6) * TC * 128 + t0 * 128 + (row & 7) * 2, pc = (row & 63) >> 3;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const uint32_t w = pack2(v[i], v[i + 1]);
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + i * 128 + ((pc ^ (i & 7)) << 4)), "h"((uint16_t)w) : "memory");
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + (i + 1) * 128 + ((pc ^ ((i + 1) & 7)) << 4)), "h"((uint16_t)(w >> 16)) : "memory");
         }
-}
+    }
+    // Rows [0, left) of a token tile to a strided tensor: by TMA where the chunk is whole, else by the warps themselves.
+    __device__ __forceinline__ void tokens_out(const CUtensorMap* m, uint32_t slot, __nv_bfloat16* dst, long long ts, int tok, int head, int img,
+                                               int left, int tid) {
+        if (left >= TC) {
+            if (issuer) {
+#pragma unroll
+                for (int c = 0; c < MV / 64; ++c) store(m, slot + c * TC * 128, c * 64, tok, head, img);
+                bulk_commit();
+            }
+            return;
+        }
+        if (issuer) bulk_commit();                     // an empty group: jobs and groups stay in step
+        for (int x = tid; x < left * (MV / 8); x += 128) {
+            const int r = x / (MV / 8), pc = x % (MV / 8);
+            const uint4 v = lds4u(slot + (pc >> 3) * TC * 128 + r * 128 + (((pc & 7) ^ (r & 7)) << 4));
+            *reinterpret_cast<uint4*>(dst + r * ts + pc * 8) = v;
+        }
+    }
+};
 
-template <int DK, int MV, bool SAVE>
-__global__ void __launch_bounds__(448, 1)
-delta_chain_tc(const __grid_constant__ TcArgs p) {
-    using L = TcChain<DK, MV, SAVE>;
+template <int DK, bool SAVE>
+__device__ __forceinline__ void chain_tc_body(const TcArgs& p, int bh) {
+    using L = TcChain<DK, SAVE>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
     const uint32_t sb = s32(smem);
-    TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::kStages * L::stage);
+    TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::kStages * L::stage + L::kSlots * MV * 128);
     const Dims& d = p.d;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bh = blockIdx.x, b = bh / d.h, h = bh % d.h;
+    const int b = bh / d.h, h = bh % d.h;
     pdl_launch_dependents();
     pdl_wait_primary();
     const int len = seq_len(d, b), nch = (len + TC - 1) / TC;
@@ -394,7 +465,7 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
             mbar_init(&ctl.empty[i], 13);
         }
         for (uint64_t* x : {&ctl.xd, &ctl.ed, &ctl.sd, &ctl.z1, &ctl.z2}) mbar_init(x, 1);
-        for (uint64_t* x : {&ctl.sp, &ctl.rp, &ctl.up}) mbar_init(x, 8);
+        for (uint64_t* x : {&ctl.spa, &ctl.sp, &ctl.rp, &ctl.up, &ctl.ur}) mbar_init(x, 8);
         for (uint64_t* x : {&ctl.z1free, &ctl.z2free, &ctl.spfree}) mbar_init(x, 4);
         fence_barrier_init();
     }
@@ -443,40 +514,33 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
     } else if (warp == 13) {
         // ---------------------------------------------------------------- products
         constexpr uint32_t id64 = idesc_bf16_f32(MV, 64, false, false), idS = idesc_bf16_f32(MV, DK, false, true);
-        constexpr int KS = DK / 16;
         bool ok = true;
         int c = 0;
         for (; c < nch; ++c) {
             const uint32_t ph = c & 1, st = sb + (c % L::kStages) * L::stage;
-            ok = full_wait(c) && mbar_wait(&ctl.sp, ph, ab);
+            ok = full_wait(c);
             if (c > 0) ok = ok && mbar_wait(&ctl.z2free, ph ^ 1, ab);          // X's place has been read out
+            ok = ok && mbar_wait(&ctl.spa, ph, ab);
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_bf16_ts(tm + L::cX, tm + L::cP + part * (DK / 2) + kk * 8,
-                                    sdesc_sw128(st + L::oK + (kk / 4) * TC * 128 + (kk % 4) * 32, 16, 1024), id64, kk > 0 || part > 0);
-                mma_commit(&ctl.xd);
+            state_product<DK>(tm + L::cX, tm + L::cP, st + L::oK, id64, 0);
+            if (DK == 128) {
+                ok = __all_sync(~0u, mbar_wait(&ctl.sp, ph, ab));
+                if (!ok) break;
+                tc_fence_after();
+                state_product<DK>(tm + L::cX, tm + L::cP, st + L::oK, id64, 1);
             }
+            if (elect_one()) mma_commit(&ctl.xd);
             __syncwarp();
             if (!SAVE) {
                 if (c > 0) ok = mbar_wait(&ctl.z1free, ph ^ 1, ab);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-                            mma_bf16_ts(tm + L::cZ, tm + L::cP + part * (DK / 2) + kk * 8,
-                                        sdesc_sw128(st + L::oQ + (kk / 4) * TC * 128 + (kk % 4) * 32, 16, 1024), id64, kk > 0 || part > 0);
-                    mma_commit(&ctl.z1);
-                }
+                state_product<DK>(tm + L::cZ, tm + L::cP, st + L::oQ, id64, 0);
+                if (DK == 128) state_product<DK>(tm + L::cZ, tm + L::cP, st + L::oQ, id64, 1);
+                if (elect_one()) mma_commit(&ctl.z1);
                 __syncwarp();
             }
             ok = mbar_wait(&ctl.rp, ph, ab);
@@ -511,13 +575,20 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
                     for (int part = 0; part < 2; ++part)
                         mma_bf16_ts(tm + L::cS, tm + L::cU + part * 32 + kk * 8, sdesc_sw128(st + L::oK + kk * 2048, TC * 128, 1024), idS, 1);
                 mma_commit(&ctl.sd);
-                if (!SAVE) {
-                    lower(tm + L::cX, tm + L::cR, st + L::oA);                 // A U, over E
-                    mma_commit(&ctl.z2);
-                }
-                mma_commit(&ctl.empty[c % L::kStages]);
+                if (SAVE) mma_commit(&ctl.empty[c % L::kStages]);
             }
             __syncwarp();
+            if (!SAVE) {
+                ok = __all_sync(~0u, mbar_wait(&ctl.ur, ph, ab));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    lower(tm + L::cX, tm + L::cR, st + L::oA);                 // A U, over E
+                    mma_commit(&ctl.z2);
+                    mma_commit(&ctl.empty[c % L::kStages]);
+                }
+                __syncwarp();
+            }
         }
         // the last products end before the CTA gives its tensor memory back
         if (!ok) {
@@ -531,8 +602,7 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
         // rows of the state: tensor-memory lane <-> row of this thread
         const int q = warp & 3;
         const uint32_t lofs = (uint32_t)(q * 32) << 16;
-        const bool active = MV == 128 || lane < 16;
-        const int row = MV == 128 ? q * 32 + lane : q * 16 + (lane & 15);
+        const int row = q * 32 + lane;
         bool ok = true;
         if (warp < 8) {
             // ------------------------------------------------------------ chain
@@ -569,9 +639,9 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
                     for (int i = 0; i < 32; ++i) w[i / 16][i % 16] = __float_as_uint(gc * v[i]);
                     tmem_st16(tm + L::cS + lofs + k0 + k, w[0]);
                     tmem_st16(tm + L::cS + lofs + k0 + k + 16, w[1]);
+                    tmem_st_wait();
+                    tc_arrive(k == 0 ? &ctl.spa : &ctl.sp, lane);
                 }
-                tmem_st_wait();
-                tc_arrive(&ctl.sp, lane);
                 // R = V - gamma X, tokens 32 hf ..
                 const int t0 = hf * 32;
                 float v[32], x[32];
@@ -605,9 +675,13 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
                     v[i] = su.x * x[i]; v[i + 1] = su.y * x[i + 1]; v[i + 2] = su.z * x[i + 2]; v[i + 3] = su.w * x[i + 3];
                 }
                 tmem_st_parts(tm + L::cU + lofs + hf * 16, tm + L::cU + 32 + lofs + hf * 16, v);
-                if (!SAVE) tmem_st_parts(tm + L::cR + lofs + hf * 16, tm + L::cR + 32 + lofs + hf * 16, x);
                 tmem_st_wait();
                 tc_arrive(&ctl.up, lane);
+                if (!SAVE) {
+                    tmem_st_parts(tm + L::cR + lofs + hf * 16, tm + L::cR + 32 + lofs + hf * 16, x);
+                    tmem_st_wait();
+                    tc_arrive(&ctl.ur, lane);
+                }
                 if (lane == 0) mbar_arrive(&ctl.empty[c % L::kStages]);
             }
             if (p.W1 && ok) {
@@ -618,52 +692,60 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
                 for (int k = 0; k < DK / 2; k += 32) {
                     float v[32];
                     tmem_ld<32>(tm + L::cS + lofs + k0 + k, v);
-                    if (active && ok)
+                    if (ok)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(o + k + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
         } else {
             // ------------------------------------------------------------ readout (or what the backward pass keeps)
+            OutRing<L::kSlots> ring{sb + L::kStages * L::stage, lane, warp == 8 && lane == 0, 0};
             for (int c = 0; c < nch; ++c) {
                 const uint32_t ph = c & 1;
                 const int left = len - c * TC;
                 const float* gam = reinterpret_cast<const float*>(smem + (c % L::kStages) * L::stage);
-                ok = full_wait(c);
+                ok = full_wait(c) && mbar_wait(SAVE ? &ctl.xd : &ctl.z1, ph, ab);
+                if (named_bar_or(3, 128, !ok)) break;
+                tc_fence_after();
+                float v[2][32];
                 if (SAVE) {
-                    if (!__all_sync(~0u, ok && mbar_wait(&ctl.xd, ph, ab))) break;
-                    tc_fence_after();
-                    __nv_bfloat16* so = p.S + ((long long)bh * d.ng + c) * 2 * state + (long long)row * DK;
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int k = 0; k < DK / 2; k += 32) {         // 32 columns of packed pairs: 64 values
-                            float v[32];
-                            tmem_ld<32>(tm + L::cP + part * (DK / 2) + lofs + k, v);
-                            if (active)
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4)
-                                    *reinterpret_cast<float4*>(so + part * state + 2 * (k + i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        for (int k = 0; k < DK / 64; ++k) {            // 32 columns of packed pairs: 64 values of the row
+                            tmem_ld<32>(tm + L::cP + part * (DK / 2) + lofs + k * 32, v[0]);
+                            if (part == 1 && k == DK / 64 - 1) tc_arrive(&ctl.spfree, lane);
+                            const uint32_t slot = ring.open();
+                            ring.put_row(slot, row, v[0]);
+                            ring.ready();
+                            if (ring.issuer) {
+                                ring.store(&p.mS, slot, k * 64, (int)((((long long)bh * d.ng + c) * 2 + part) * d.dv), 0, 0);
+                                bulk_commit();
+                            }
                         }
-                    tc_arrive(&ctl.spfree, lane);
-                    if (!__all_sync(~0u, mbar_wait(&ctl.ed, ph, ab))) break;
+                    ok = mbar_wait(&ctl.ed, ph, ab);
+                    if (named_bar_or(3, 128, !ok)) break;
                     tc_fence_after();
-                    float v[2][32];
                     tmem_ld<32>(tm + L::cX + lofs, v[0]);
                     tmem_ld<32>(tm + L::cX + lofs + 32, v[1]);
                     tc_arrive(&ctl.z2free, lane);
-                    __nv_bfloat16* eo = p.E + ((long long)bh * d.N + (long long)c * TC) * d.dv + row;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        put_column(eo + e * 32 * d.dv, d.dv, v[e], left - e * 32, active);
+                    for (int part = 0; part < 2; ++part) {
+                        const uint32_t slot = ring.open();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[e][i] -= lo_f(pack2(v[e][i], 0.f));
-                        put_column(eo + p.e_ps + e * 32 * d.dv, d.dv, v[e], left - e * 32, active);
+                        for (int e = 0; e < 2; ++e) {
+                            ring.put_column(slot, row, e * 32, v[e]);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[e][i] -= lo_f(pack2(v[e][i], 0.f));
+                        }
+                        ring.ready();
+                        if (ring.issuer) {
+#pragma unroll
+                            for (int k = 0; k < MV / 64; ++k) ring.store(&p.mE, slot + k * TC * 128, k * 64, c * TC, bh, part);
+                            bulk_commit();
+                        }
                     }
                 } else {
-                    if (!__all_sync(~0u, ok && mbar_wait(&ctl.z1, ph, ab))) break;
-                    tc_fence_after();
-                    float v[2][32];
                     tmem_ld<32>(tm + L::cZ + lofs, v[0]);
                     tmem_ld<32>(tm + L::cZ + lofs + 32, v[1]);
                     tc_arrive(&ctl.z1free, lane);
@@ -674,22 +756,27 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
                             const float4 g = *reinterpret_cast<const float4*>(gam + e * 32 + i);
                             v[e][i] *= d.scale * g.x; v[e][i + 1] *= d.scale * g.y; v[e][i + 2] *= d.scale * g.z; v[e][i + 3] *= d.scale * g.w;
                         }
-                    if (!__all_sync(~0u, mbar_wait(&ctl.z2, ph, ab))) break;
+                    ok = mbar_wait(&ctl.z2, ph, ab);
+                    if (named_bar_or(3, 128, !ok)) break;
                     tc_fence_after();
-                    __nv_bfloat16* zo = reinterpret_cast<__nv_bfloat16*>(p.Z.p) + b * p.Z.bs + h * p.Z.hs + (long long)c * TC * p.Z.ts + row;
                     float x[2][32];
                     tmem_ld<32>(tm + L::cX + lofs, x[0]);
                     tmem_ld<32>(tm + L::cX + lofs + 32, x[1]);
                     tc_arrive(&ctl.z2free, lane);
+                    const uint32_t slot = ring.open();
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[e][i] += v[e][i];
-                        put_column(zo + e * 32 * p.Z.ts, p.Z.ts, x[e], left - e * 32, active);
+                        ring.put_column(slot, row, e * 32, x[e]);
                     }
+                    ring.ready();
+                    ring.tokens_out(&p.mZ, slot, reinterpret_cast<__nv_bfloat16*>(p.Z.p) + b * p.Z.bs + h * p.Z.hs + (long long)c * TC * p.Z.ts, p.Z.ts,
+                                    c * TC, h * p.zh, b * p.zb, left, tid - 256);
                 }
                 if (lane == 0) mbar_arrive(&ctl.empty[c % L::kStages]);
             }
+            if (ring.issuer) bulk_wait<0>();
         }
     }
     __syncthreads();
@@ -703,26 +790,25 @@ delta_chain_tc(const __grid_constant__ TcArgs p) {
 //   D -> parts | X = D K^T, AO = dZ^T A | dU = suffix X + AO -> parts | Y = T_u^T dU | -gamma beta Y -> parts
 //   D = gamma_C D + (scale gamma dZ)^T Q - (gamma beta Y)^T K
 // The four output warps turn dZ into the scaled left operand one step ahead, and write D, Y and dV.
-template <int DK, int MV>
+template <int DK>
 struct TcReverse {
     static constexpr int oA = kTcGates, oU = oA + kTcMat, oK = oU + kTcMat, oQ = oK + DK * 128, oO = oQ + DK * 128;
-    static constexpr int stage = oO + MV * 128, kStages = 2;
-    static constexpr int used = kStages * stage + 512 + 1024, smem = used > 116 * 1024 ? used : 116 * 1024;   // one CTA per SM
+    static constexpr int stage = oO + MV * 128, kStages = 2, kSlots = 3;
+    static constexpr int used = kStages * stage + kSlots * MV * 128 + 512 + 1024, smem = used > 116 * 1024 ? used : 116 * 1024;   // one CTA per SM
     static_assert(smem <= 227 * 1024 && stage % 1024 == 0, "shared memory of a reverse CTA");
     static constexpr uint32_t cS = 0, cP = DK, cX = 2 * DK, cA = cX + 64, cR = cA + 64, cF = cR + 64;
 };
 
-template <int DK, int MV>
-__global__ void __launch_bounds__(448, 1)
-delta_reverse_tc(const __grid_constant__ TcArgs p) {
-    using L = TcReverse<DK, MV>;
+template <int DK>
+__device__ __forceinline__ void reverse_tc_body(const TcArgs& p, int bh) {
+    using L = TcReverse<DK>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
     const uint32_t sb = s32(smem);
-    TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::kStages * L::stage);
+    TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::kStages * L::stage + L::kSlots * MV * 128);
     const Dims& d = p.d;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bh = blockIdx.x, b = bh / d.h, h = bh % d.h;
+    const int b = bh / d.h, h = bh % d.h;
     pdl_launch_dependents();
     pdl_wait_primary();
     const int len = seq_len(d, b), nch = (len + TC - 1) / TC;
@@ -735,7 +821,7 @@ delta_reverse_tc(const __grid_constant__ TcArgs p) {
             mbar_init(&ctl.empty[i], 13);
         }
         for (uint64_t* x : {&ctl.xd, &ctl.ed, &ctl.sd, &ctl.z1}) mbar_init(x, 1);
-        for (uint64_t* x : {&ctl.sp, &ctl.rp, &ctl.up}) mbar_init(x, 8);
+        for (uint64_t* x : {&ctl.spa, &ctl.sp, &ctl.rp, &ctl.up}) mbar_init(x, 8);
         for (uint64_t* x : {&ctl.z2free, &ctl.spfree, &ctl.fr}) mbar_init(x, 4);
         fence_barrier_init();
     }
@@ -802,20 +888,19 @@ delta_reverse_tc(const __grid_constant__ TcArgs p) {
                 }
             }
             __syncwarp();
-            ok = mbar_wait(&ctl.sp, ph, ab);
+            ok = mbar_wait(&ctl.spa, ph, ab);
             if (k > 0) ok = ok && mbar_wait(&ctl.z2free, ph ^ 1, ab);          // Y has been read out
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_bf16_ts(tm + L::cX, tm + L::cP + part * (DK / 2) + kk * 8,
-                                    sdesc_sw128(st + L::oK + (kk / 4) * TC * 128 + (kk % 4) * 32, 16, 1024), id64, kk > 0 || part > 0);
-                mma_commit(&ctl.xd);
+            state_product<DK>(tm + L::cX, tm + L::cP, st + L::oK, id64, 0);
+            if (DK == 128) {
+                ok = __all_sync(~0u, mbar_wait(&ctl.sp, ph, ab));
+                if (!ok) break;
+                tc_fence_after();
+                state_product<DK>(tm + L::cX, tm + L::cP, st + L::oK, id64, 1);
             }
+            if (elect_one()) mma_commit(&ctl.xd);
             __syncwarp();
             ok = __all_sync(~0u, mbar_wait(&ctl.rp, ph, ab));
             if (!ok) break;
@@ -868,8 +953,7 @@ delta_reverse_tc(const __grid_constant__ TcArgs p) {
     } else {
         const int q = warp & 3;
         const uint32_t lofs = (uint32_t)(q * 32) << 16;
-        const bool active = MV == 128 || lane < 16;
-        const int row = MV == 128 ? q * 32 + lane : q * 16 + (lane & 15);
+        const int row = q * 32 + lane;
         bool ok = true;
         if (warp < 8) {
             // ------------------------------------------------------------ chain
@@ -904,9 +988,9 @@ delta_reverse_tc(const __grid_constant__ TcArgs p) {
                     for (int i = 0; i < 32; ++i) w[i / 16][i % 16] = __float_as_uint(gc * v[i]);
                     tmem_st16(tm + L::cS + lofs + k0 + j, w[0]);
                     tmem_st16(tm + L::cS + lofs + k0 + j + 16, w[1]);
+                    tmem_st_wait();
+                    tc_arrive(j == 0 ? &ctl.spa : &ctl.sp, lane);
                 }
-                tmem_st_wait();
-                tc_arrive(&ctl.sp, lane);
                 const int t0 = hf * 32;
                 float v[32], x[32];
                 if (!__all_sync(~0u, mbar_wait(&ctl.xd, ph, ab))) { ok = false; break; }
@@ -945,75 +1029,116 @@ delta_reverse_tc(const __grid_constant__ TcArgs p) {
                 for (int j = 0; j < DK / 2; j += 32) {
                     float v[32];
                     tmem_ld<32>(tm + L::cS + lofs + k0 + j, v);
-                    if (active && ok)
+                    if (ok)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(o + j + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
         } else {
             // ------------------------------------------------------------ scaled dZ, and what the step gives
-            for (int k = 0; k < nch; ++k) {
-                const uint32_t ph = k & 1;
-                const int c = nch - 1 - k, left = len - c * TC;
+            OutRing<L::kSlots> ring{sb + L::kStages * L::stage, lane, warp == 8 && lane == 0, 0};
+            // scale gamma dZ of step k, as parts
+            auto scaled = [&](int k) {
+                const int left = len - (nch - 1 - k) * TC;
                 const uint8_t* st = smem + (k % L::kStages) * L::stage;
                 const float* gam = reinterpret_cast<const float*>(st);
                 ok = full_wait(k);
-                if (k > 0) ok = ok && mbar_wait(&ctl.z1, ph ^ 1, ab);
-                if (!__all_sync(~0u, ok)) break;
+                if (k > 0) ok = ok && mbar_wait(&ctl.z1, (k - 1) & 1, ab);     // the step before has used its own
+                if (named_bar_or(3, 128, !ok)) return false;
                 tc_fence_after();
-                float v[2][32];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const uint32_t x = *reinterpret_cast<const uint16_t*>(st + L::oO + (row >> 6) * TC * 128 + (e * 32 + i) * 128 +
                                                                                ((((row & 63) >> 3) ^ (i & 7)) << 4) + (row & 7) * 2);
-                        v[e][i] = e * 32 + i < left ? __uint_as_float(x << 16) * (d.scale * gam[e * 32 + i]) : 0.f;
+                        v[i] = e * 32 + i < left ? __uint_as_float(x << 16) * (d.scale * gam[e * 32 + i]) : 0.f;
                     }
-                    tmem_st_parts(tm + L::cF + lofs + e * 16, tm + L::cF + 32 + lofs + e * 16, v[e]);
+                    tmem_st_parts(tm + L::cF + lofs + e * 16, tm + L::cF + 32 + lofs + e * 16, v);
                 }
                 tmem_st_wait();
                 tc_arrive(&ctl.fr, lane);
-                if (!__all_sync(~0u, mbar_wait(&ctl.xd, ph, ab))) break;
+                return true;
+            };
+            bool go = nch > 0 && scaled(0);
+            for (int k = 0; go && k < nch; ++k) {
+                const uint32_t ph = k & 1;
+                const int c = nch - 1 - k, left = len - c * TC;
+                const float* gam = reinterpret_cast<const float*>(smem + (k % L::kStages) * L::stage);
+                float v[2][32];
+                ok = mbar_wait(&ctl.xd, ph, ab);
+                if (named_bar_or(3, 128, !ok)) break;
                 tc_fence_after();
-                __nv_bfloat16* so = p.S + ((long long)bh * d.ng + c) * 2 * state + (long long)row * DK;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int j = 0; j < DK / 2; j += 32) {
-                        float x[32];
-                        tmem_ld<32>(tm + L::cP + part * (DK / 2) + lofs + j, x);
-                        if (active)
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4*>(so + part * state + 2 * (j + i)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    for (int j = 0; j < DK / 64; ++j) {
+                        tmem_ld<32>(tm + L::cP + part * (DK / 2) + lofs + j * 32, v[0]);
+                        if (part == 1 && j == DK / 64 - 1) tc_arrive(&ctl.spfree, lane);
+                        const uint32_t slot = ring.open();
+                        ring.put_row(slot, row, v[0]);
+                        ring.ready();
+                        if (ring.issuer) {
+                            ring.store(&p.mS, slot, j * 64, (int)((((long long)bh * d.ng + c) * 2 + part) * d.dv), 0, 0);
+                            bulk_commit();
+                        }
                     }
-                tc_arrive(&ctl.spfree, lane);
-                if (!__all_sync(~0u, mbar_wait(&ctl.ed, ph, ab))) break;
+                if (k + 1 < nch && !(go = scaled(k + 1))) break;
+                ok = mbar_wait(&ctl.ed, ph, ab);
+                if (named_bar_or(3, 128, !ok)) break;
                 tc_fence_after();
                 tmem_ld<32>(tm + L::cX + lofs, v[0]);
                 tmem_ld<32>(tm + L::cX + lofs + 32, v[1]);
                 tc_arrive(&ctl.z2free, lane);
-                __nv_bfloat16* yo = p.E + ((long long)bh * d.N + (long long)c * TC) * d.dv + row;
-                __nv_bfloat16* vo = reinterpret_cast<__nv_bfloat16*>(p.Z.p) + b * p.Z.bs + h * p.Z.hs + (long long)c * TC * p.Z.ts + row;
+                {
+                    const uint32_t slot = ring.open();
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x[32];
-                    put_column(yo + e * 32 * d.dv, d.dv, v[e], left - e * 32, active);
+                    for (int e = 0; e < 2; ++e) {
+                        float x[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        x[i] = gam[2 * TC + e * 32 + i] * v[e][i];
-                        v[e][i] -= lo_f(pack2(v[e][i], 0.f));
+                        for (int i = 0; i < 32; ++i) x[i] = gam[2 * TC + e * 32 + i] * v[e][i];
+                        ring.put_column(slot, row, e * 32, x);
                     }
-                    put_column(vo + e * 32 * p.Z.ts, p.Z.ts, x, left - e * 32, active);
-                    put_column(yo + p.e_ps + e * 32 * d.dv, d.dv, v[e], left - e * 32, active);
+                    ring.ready();
+                    ring.tokens_out(&p.mZ, slot, reinterpret_cast<__nv_bfloat16*>(p.Z.p) + b * p.Z.bs + h * p.Z.hs + (long long)c * TC * p.Z.ts, p.Z.ts,
+                                    c * TC, h * p.zh, b * p.zb, left, tid - 256);
+                }
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const uint32_t slot = ring.open();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        ring.put_column(slot, row, e * 32, v[e]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[e][i] -= lo_f(pack2(v[e][i], 0.f));
+                    }
+                    ring.ready();
+                    if (ring.issuer) {
+#pragma unroll
+                        for (int j = 0; j < MV / 64; ++j) ring.store(&p.mE, slot + j * TC * 128, j * 64, c * TC, bh, part);
+                        bulk_commit();
+                    }
                 }
                 if (lane == 0) mbar_arrive(&ctl.empty[k % L::kStages]);
             }
+            if (ring.issuer) bulk_wait<0>();
         }
     }
     __syncthreads();
     if (warp == 13) tmem_dealloc(ctl.tmem, 512);
+}
+
+template <int DK>
+__global__ void __launch_bounds__(448, 1) delta_chain_tc(const __grid_constant__ TcArgs p) {
+    chain_tc_body<DK, false>(p, blockIdx.x);
+}
+// The backward pass's two sequential sweeps need nothing of each other: one launch, the longer ones first.
+template <int DK>
+__global__ void __launch_bounds__(448, 1) delta_both_tc(const __grid_constant__ TcArgs chain, const __grid_constant__ TcArgs reverse) {
+    const int n = chain.d.B * chain.d.h;
+    if ((int)blockIdx.x < n) reverse_tc_body<DK>(reverse, blockIdx.x);
+    else chain_tc_body<DK, true>(chain, blockIdx.x - n);
 }
 
 // --------------------------------------------------------------------------------------------------
@@ -1042,6 +1167,21 @@ static bool tc_args(TcArgs* a, const Call& c, bool backward, uint8_t* rec) {
     return map64(&a->K, bf16_parts(c.K), c.d, c.d.hk, c.d.dk) && map64(&a->Q, bf16_parts(c.Q), c.d, c.d.hk, c.d.dk) &&
            map64(&a->V, bf16_parts(c.V), c.d, c.d.h, c.d.dv);
 }
+// The maps of a kernel's outputs: Z (or dV), and in the backward pass E (or Y) and the states (or adjoints).
+static bool tc_outputs(TcArgs* a, const View& z, const Dims& d, __nv_bfloat16* E, long long e_ps, __nv_bfloat16* S) {
+    a->Z = z;
+    a->zh = z.hs != 0;
+    a->zb = z.bs != 0;
+    bool ok = encode_map(&a->mZ, z.p, 2, {(cuuint64_t)d.dv, (cuuint64_t)d.N, (cuuint64_t)(z.hs ? d.h : 1), (cuuint64_t)(z.bs ? d.B : 1), 1},
+                         {z.ts ? z.ts : d.dv, z.hs ? z.hs : d.dv, z.bs ? z.bs : d.dv, d.dv}, 128, TC);
+    if (E) {
+        const long long srows = (long long)d.B * d.h * d.ng * 2 * d.dv;
+        ok = ok && srows < (1LL << 31) &&
+             encode_map(&a->mE, E, 2, {(cuuint64_t)d.dv, (cuuint64_t)d.N, (cuuint64_t)d.B * d.h, 2, 1}, {d.dv, (long long)d.N * d.dv, e_ps, e_ps}, 128, TC) &&
+             encode_map2(&a->mS, S, d.dk, srows, d.dv);
+    }
+    return ok;
+}
 template <int DK, bool BACKWARD>
 static ttt_status run_prep64(const Call& c, uint8_t* rec) {
     using L = Prep64<DK, BACKWARD>;
@@ -1051,21 +1191,17 @@ static ttt_status run_prep64(const Call& c, uint8_t* rec) {
     const long long n = (long long)c.d.B * c.d.h * ((c.d.N + TC - 1) / TC);
     return launch(k, n, 128, L::smem, c.stream, c.d, bf16_parts(c.Q), bf16_parts(c.K), c.G, c.Beta, rec, error_word(c));
 }
-template <int DK, int MV, bool SAVE>
+template <int DK>
 static ttt_status run_chain_tc(const Call& c, const TcArgs& a) {
-    constexpr auto k = delta_chain_tc<DK, MV, SAVE>;
-    ttt_status st = allow_smem<k>(TcChain<DK, MV, SAVE>::smem);
-    if (st != TTT_OK) return st;
-    return launch(k, c.d.B * c.d.h, 448, TcChain<DK, MV, SAVE>::smem, c.stream, a);
+    constexpr auto k = delta_chain_tc<DK>;
+    constexpr int smem = TcChain<DK, false>::smem;
+    const ttt_status st = allow_smem<k>(smem);
+    return st != TTT_OK ? st : launch(k, c.d.B * c.d.h, 448, smem, c.stream, a);
 }
-template <int DK, int MV>
-static ttt_status run_reverse_tc(const Call& c, const TcArgs& a) {
-    constexpr auto k = delta_reverse_tc<DK, MV>;
-    ttt_status st = allow_smem<k>(TcReverse<DK, MV>::smem);
-    if (st != TTT_OK) return st;
-    return launch(k, c.d.B * c.d.h, 448, TcReverse<DK, MV>::smem, c.stream, a);
-}
-template <int DK, bool SAVE>
-static ttt_status chain_tc(const Call& c, const TcArgs& a) {
-    return c.d.dv == 64 ? run_chain_tc<DK, 64, SAVE>(c, a) : run_chain_tc<DK, 128, SAVE>(c, a);
+template <int DK>
+static ttt_status run_both_tc(const Call& c, const TcArgs& chain, const TcArgs& reverse) {
+    constexpr auto k = delta_both_tc<DK>;
+    constexpr int smem = std::max(TcChain<DK, true>::smem, TcReverse<DK>::smem);
+    const ttt_status st = allow_smem<k>(smem);
+    return st != TTT_OK ? st : launch(k, 2LL * c.d.B * c.d.h, 448, smem, c.stream, chain, reverse);
 }

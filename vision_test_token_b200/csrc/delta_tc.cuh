@@ -52,36 +52,38 @@ __device__ __forceinline__ void tma_load_5d_at(uint32_t dst, const CUtensorMap* 
 // --------------------------------------------------------------------------------------------------
 // Prep: the 64 x 64 matrices.  One CTA of four warps per chunk.
 // --------------------------------------------------------------------------------------------------
-constexpr int GP2 = TC + 4, BP2 = CT + 4;     // row pitches (floats) of the 64 x 64 and the 32 x 32 matrices
+constexpr int GP2 = TC + 4;                   // row pitch (floats) of the 64 x 64 matrices
 
 template <int DK, bool BACKWARD>
 struct Prep64 {
-    static constexpr int KP = DK + 8;
-    static constexpr int tiles = 2 * TC * KP * 2, mats = 2 * TC * GP2 * 4;
-    static constexpr int front = tiles > mats ? tiles : mats;  // K and Q tiles, then G and Q K^T (then the blocks)
-    static constexpr int blocks = (BACKWARD ? 6 : 3) * CT * BP2 * 4;               // diagonal inverses and a product, per inverse
-    static constexpr int extra = blocks > TC * GP2 * 4 ? blocks - TC * GP2 * 4 : 0;   // what Q K^T's place does not hold
-    static constexpr int oImg = (front + extra + 127) / 128 * 128;
-    static constexpr int oRow = oImg + kTcMat;                 // one image at a time; g, beta, suffix inside 32
+    static constexpr int KP = DK + 8, mat = TC * GP2 * 4;
+    static constexpr int tiles = 2 * TC * KP * 2;
+    static constexpr int front = tiles > 2 * mat ? tiles : 2 * mat;                // K and Q tiles, then G and Q K^T, then G and T'
+    static constexpr int oU = (front + 127) / 128 * 128, oImg = oU + (BACKWARD ? mat : 0);   // T_u; one image at a time
+    static constexpr int oRow = oImg + kTcMat;                 // g, beta, suffix inside 16
     static constexpr int smem = oRow + 3 * TC * 4;
 };
 
-// Element (i, j) of a two-part 64 x 64 image.
-__device__ __forceinline__ void put_img(uint8_t* img, int i, int j, float x) {
-    const uint32_t w = pack2(x, 0.f);
+// Elements (i, j) and (i, j + 1), j even, of a two-part 64 x 64 image.
+__device__ __forceinline__ void put_pair(uint8_t* img, int i, int j, float x, float y) {
+    uint32_t w[2];
+    split2<2>(x, y, w);
     uint8_t* o = img + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
-    *reinterpret_cast<uint16_t*>(o) = (uint16_t)w;
-    *reinterpret_cast<uint16_t*>(o + TC * 128) = (uint16_t)pack2(x - lo_f(w), 0.f);
+    *reinterpret_cast<uint32_t*>(o) = w[0];
+    *reinterpret_cast<uint32_t*>(o + TC * 128) = w[1];
 }
 
-// Column `lane` of (I + L)^{-1} for a 32 x 32 block, L_il = left_i G_il right_l; out [32][BP2].
-__device__ __forceinline__ void solve32(const float* g, float left, float right, float* out, int lane) {
-    float y[CT];
+// Inverses of I + L, L = G diag(beta) (T', lanes 0-15) and diag(beta) G (T_u, lanes 16-31), for a 16 x 16 diagonal block
+// of G: a column per lane, by forward substitution.
+__device__ __forceinline__ void solve16(const float* g, const float* beta, float* out, int lane) {
+    const bool u = lane >= 16;
+    const int col = lane & 15;
+    float y[16];
 #pragma unroll
-    for (int i = 0; i < CT; ++i) {
+    for (int i = 0; i < 16; ++i) {
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int l = 0; l < CT; l += 4) {
+        for (int l = 0; l < 16; l += 4) {
             if (l >= i) continue;
             const float4 v = *reinterpret_cast<const float4*>(g + i * GP2 + l);
             s[0] = fmaf(v.x, y[l], s[0]);
@@ -89,30 +91,113 @@ __device__ __forceinline__ void solve32(const float* g, float left, float right,
             if (l + 2 < i) s[2] = fmaf(v.z, y[l + 2], s[2]);
             if (l + 3 < i) s[3] = fmaf(v.w, y[l + 3], s[3]);
         }
-        const float x = (i == lane ? 1.f : 0.f) - __shfl_sync(~0u, left, i) * ((s[0] + s[1]) + (s[2] + s[3]));
-        out[i * BP2 + lane] = x;
-        y[i] = x * __shfl_sync(~0u, right, i);
+        const float be = beta[i], sum = (s[0] + s[1]) + (s[2] + s[3]);
+        const float x = (i == col ? 1.f : 0.f) - (u ? be * sum : sum);
+        if (out) out[i * GP2 + col] = i >= col ? x : 0.f;
+        y[i] = u ? x : be * x;
     }
 }
-// Rows 8 w .. 8 w + 7, column `lane` of A B, or of A diag(right) B (32 x 32 each).
-template <bool SCALE>
-__device__ __forceinline__ void mul32(float (&c)[8], const float* a, int pitch, const float* right, const float* b, int w, int lane) {
+// The block below two inverted diagonal blocks of 16 KS: acc = T_22 L_21 T_11, rows 16 strip .., columns col0 .. col0 + 15
+// (U: of T_u, else of T').  The first product's accumulators are the second one's left operand.  Operands as two
+// bf16 parts, the product of the low ones dropped: about 16 bits, as the inverse is handed on.
+template <int KS, bool U>
+__device__ __forceinline__ void below(float (&acc)[2][4], const float* g21, const float* beta1, const float* beta2, const float* t22,
+                                      const float* t11, int strip, int col0, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t m[KS][2][4];                          // T_22 L_21 as parts, [16 columns][part]
+    {
+        float c[2 * KS][4] = {};
 #pragma unroll
-    for (int r = 0; r < 8; ++r) c[r] = 0.f;
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks > strip) continue;              // T_22 is lower triangular
+            uint32_t a[2][4];
 #pragma unroll
-    for (int l = 0; l < CT; l += 4) {
-        float x[4];
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = *reinterpret_cast<const float2*>(t22 + (strip * 16 + g + (e & 1) * 8) * GP2 + ks * 16 + 2 * t + (e >> 1) * 8);
+                uint32_t w[2];
+                split2<2>(v.x, v.y, w);
+                a[0][e] = w[0];
+                a[1][e] = w[1];
+            }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = b[(l + k) * BP2 + lane];
-        if (SCALE) {
-            const float4 s = *reinterpret_cast<const float4*>(right + l);
-            x[0] *= s.x; x[1] *= s.y; x[2] *= s.z; x[3] *= s.w;
+            for (int n = 0; n < 2 * KS; ++n) {
+                uint32_t b[2][2];
+                const float right = U ? 1.f : beta1[n * 8 + g];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = ks * 16 + 2 * t + e * 8;
+                    const float2 left = U ? *reinterpret_cast<const float2*>(beta2 + k) : make_float2(right, right);
+                    uint32_t w[2];
+                    split2<2>(left.x * g21[k * GP2 + n * 8 + g], left.y * g21[(k + 1) * GP2 + n * 8 + g], w);
+                    b[0][e] = w[0];
+                    b[1][e] = w[1];
+                }
+                mma16816(c[n], a[0], b[0][0], b[0][1]);
+                mma16816(c[n], a[0], b[1][0], b[1][1]);
+                mma16816(c[n], a[1], b[0][0], b[0][1]);
+            }
         }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const float4 v = *reinterpret_cast<const float4*>(a + (w * 8 + r) * pitch + l);
-            c[r] = fmaf(v.x, x[0], fmaf(v.y, x[1], fmaf(v.z, x[2], fmaf(v.w, x[3], c[r]))));
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w[2];
+                split2<2>(c[2 * ks + (e >> 1)][(e & 1) * 2], c[2 * ks + (e >> 1)][(e & 1) * 2 + 1], w);
+                m[ks][0][e] = w[0];
+                m[ks][1][e] = w[1];
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t b[2][2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float* x = t11 + (ks * 16 + 2 * t + e * 8) * GP2 + col0 + n * 8 + g;
+                uint32_t w[2];
+                split2<2>(x[0], x[GP2], w);
+                b[0][e] = w[0];
+                b[1][e] = w[1];
+            }
+            mma16816(acc[n], m[ks][0], b[0][0], b[0][1]);
+            mma16816(acc[n], m[ks][0], b[1][0], b[1][1]);
+            mma16816(acc[n], m[ks][1], b[0][0], b[0][1]);
         }
+    }
+}
+// Joins the four 16 x 16 blocks on the diagonal of a 64 x 64 inverse at t (fp32, zeros above) pair by pair ..
+template <bool U>
+__device__ __forceinline__ void join16(const float* gm, const float* beta, float* t, int pair, int lane) {
+    const int o = pair * 32;
+    float acc[2][4];
+    below<1, U>(acc, gm + (o + 16) * GP2 + o, beta + o, beta + o + 16, t + (o + 16) * GP2 + o + 16, t + o * GP2 + o, 0, 0, lane);
+    float* x = t + (o + 16 + (lane >> 2)) * GP2 + o + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        *reinterpret_cast<float2*>(x + n * 8) = make_float2(-acc[n][0], -acc[n][1]);
+        *reinterpret_cast<float2*>(x + n * 8 + 8 * GP2) = make_float2(-acc[n][2], -acc[n][3]);
+    }
+}
+// .. and writes the whole inverse, its last block among it, as an image.
+template <bool U>
+__device__ __forceinline__ void join32(const float* gm, const float* beta, const float* t, uint8_t* img, int warp, int lane) {
+    const int strip = warp >> 1, col0 = (warp & 1) * 16;
+    float acc[2][4];
+    below<2, U>(acc, gm + 32 * GP2, beta, beta + 32, t + 32 * GP2 + 32, t, strip, col0, lane);
+    const int i = 32 + strip * 16 + (lane >> 2), j = col0 + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        put_pair(img, i, j + n * 8, -acc[n][0], -acc[n][1]);
+        put_pair(img, i + 8, j + n * 8, -acc[n][2], -acc[n][3]);
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const int x = warp * 16 + r * 2 + (lane >> 4), y = (x & 32) + (lane & 15) * 2;
+        const float2 v = *reinterpret_cast<const float2*>(t + x * GP2 + y);
+        put_pair(img, x, y, v.x, v.y);
     }
 }
 
@@ -133,10 +218,11 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
     const uint32_t kt = s32(smem), qt = kt + TC * KP * 2;
     float* kkm = reinterpret_cast<float*>(smem);
     float* qkm = kkm + TC * GP2;
-    float* blk = qkm;                                          // T'_11, T'_22, product (, the same of T_u) once Q K^T is used up
+    float* tm = qkm;                                           // T', once Q K^T is used up
+    float* um = reinterpret_cast<float*>(smem + L::oU);
     uint8_t* img = smem + L::oImg;
     float* gr = reinterpret_cast<float*>(smem + L::oRow);
-    float *br = gr + TC, *s32r = br + TC;
+    float *br = gr + TC, *s16 = br + TC;
     {
         const char* ks = reinterpret_cast<const char*>(K.p + b * K.bs + (h / d.r) * K.hs + (long long)c * TC * K.ts);
         const char* qs = reinterpret_cast<const char*>(Q.p + b * Q.bs + (h / d.r) * Q.hs + (long long)c * TC * Q.ts);
@@ -158,22 +244,28 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
         const long long tok = (long long)c * TC + t;
         const float g = live ? reinterpret_cast<const float*>(G.p)[b * G.bs + h * G.hs + tok * G.ts] : 0.f;
         const float beta = live ? reinterpret_cast<const float*>(Beta.p)[b * Beta.bs + h * Beta.hs + tok * Beta.ts] : 0.f;
-        float pre = g, suf = __shfl_down_sync(~0u, g, 1);
-        if (lane == 31) suf = 0.f;
+        const int l16 = lane & 15;
+        float pre = g, suf = __shfl_down_sync(~0u, g, 1, 16);
+        if (l16 == 15) suf = 0.f;
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const float a = __shfl_up_sync(~0u, pre, o), z = __shfl_down_sync(~0u, suf, o);
-            if (lane >= o) pre += a;
-            if (lane + o < 32) suf += z;
+        for (int o = 1; o < 16; o *= 2) {
+            const float a = __shfl_up_sync(~0u, pre, o, 16), z = __shfl_down_sync(~0u, suf, o, 16);
+            if (l16 >= o) pre += a;
+            if (l16 + o < 16) suf += z;
         }
         gr[t] = g;
         br[t] = beta;
-        s32r[t] = suf;
+        s16[t] = suf;
         asm volatile("bar.sync 1, 64;" ::: "memory");
-        const float other = warp ? gr[0] + s32r[0] : gr[32] + s32r[32];     // the other half's sum
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {                          // the other sixteens' sums
+            const float all = gr[q * 16] + s16[q * 16];
+            if (q < t / 16) pre += all;
+            if (q > t / 16) suf += all;
+        }
         float* gates = reinterpret_cast<float*>(out);
-        gates[t] = expf(warp ? other + pre : pre);
-        gates[TC + t] = expf(warp ? suf : suf + other);
+        gates[t] = expf(pre);
+        gates[TC + t] = expf(suf);
         gates[2 * TC + t] = beta;
     }
     for (int x = tid; x < kTcMat / 16; x += 128) reinterpret_cast<uint4*>(img)[x] = make_uint4(0, 0, 0, 0);   // what lies above the diagonal
@@ -213,9 +305,11 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float* o = (e ? qkm : kkm) + ((e ? 3 - warp : warp) * 16 + g) * GP2 + 2 * t;
+            const int block = e ? 3 - warp : warp;
+            float* o = (e ? qkm : kkm) + (block * 16 + g) * GP2 + 2 * t;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
+                if (n > 2 * block + 1) continue;
                 *reinterpret_cast<float2*>(o + n * 8) = make_float2(m[e][n][0], m[e][n][1]);
                 *reinterpret_cast<float2*>(o + 8 * GP2 + n * 8) = make_float2(m[e][n][2], m[e][n][3]);
             }
@@ -223,58 +317,54 @@ delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t
     }
     __syncthreads();
     {
-        // Gamma by 32 x 32 blocks, a column per lane, logs summed from zero at i = j: warp 0 rows 0-31 of columns 0-31,
-        // warp 1 rows 32-63 of columns 32-63, warps 2 and 3 sixteen rows each of the block below the diagonal
-        const int j = (warp == 1 ? 32 : 0) + lane;
-        const int i0 = warp == 0 ? 0 : warp == 3 ? 48 : 32, n = warp < 2 ? 32 : 16;
-        float s = 0.f;
-        if (warp >= 2) s = s32r[j];
-        if (warp == 3)
-            for (int k = 32; k < 48; ++k) s += gr[k];
+        // Gamma: warp w takes rows 16 w .. 16 w + 15, a lane two columns; logs summed from zero at i = j
+        const int j = 2 * lane, jb = lane >> 3;
+        float s0 = 0.f, s1 = 0.f;
+        if (jb < warp) {
+            s0 = s16[j];
+            s1 = s16[j + 1];
+            for (int q = jb + 1; q < warp; ++q) {
+                const float all = gr[q * 16] + s16[q * 16];
+                s0 += all;
+                s1 += all;
+            }
+        }
+        if (jb <= warp) {
 #pragma unroll 4
-        for (int i = i0; i < i0 + n; ++i) {
-            if (i > j) s += gr[i];
-            const float dec = i >= j ? __expf(s) : 0.f;        // relative error about 2^-22 (1 + |s|)
-            if (i >= j) put_img(img, i, j, d.scale * dec * qkm[i * GP2 + j]);
-            kkm[i * GP2 + j] = i > j ? dec * kkm[i * GP2 + j] : 0.f;
+            for (int i = warp * 16; i < warp * 16 + 16; ++i) {
+                const float gi = gr[i];
+                if (i > j) s0 += gi;
+                if (i > j + 1) s1 += gi;
+                const float d0 = i >= j ? __expf(s0) : 0.f, d1 = i > j ? __expf(s1) : 0.f;      // relative error about 2^-22 (1 + |s|)
+                float2* kk = reinterpret_cast<float2*>(kkm + i * GP2 + j);
+                const float2 a = *reinterpret_cast<const float2*>(qkm + i * GP2 + j), x = *kk;
+                put_pair(img, i, j, i >= j ? d.scale * d0 * a.x : 0.f, i > j ? d.scale * d1 * a.y : 0.f);
+                *kk = make_float2(i > j ? d0 * x.x : 0.f, i > j + 1 ? d1 * x.y : 0.f);
+            }
         }
     }
     __syncthreads();
     copy_out(1);                                               // A
-    const int nb = CT * BP2;
-    const float b0 = br[lane], b1 = br[32 + lane];
-    // diagonal blocks: T' = (I + G beta)^{-1} (warps 0, 1), T_u = (I + beta G)^{-1} (warps 2, 3)
-    if (warp == 0) solve32(kkm, 1.f, b0, blk, lane);
-    if (warp == 1) solve32(kkm + 32 * GP2 + 32, 1.f, b1, blk + nb, lane);
-    if (BACKWARD && warp == 2) solve32(kkm, b0, 1.f, blk + 3 * nb, lane);
-    if (BACKWARD && warp == 3) solve32(kkm + 32 * GP2 + 32, b1, 1.f, blk + 4 * nb, lane);
-    __syncthreads();
-    // the block below: - T'_22 (G_21 beta_1 T'_11), and - T_u22 (beta_2 G_21 T_u11)
-    float p[8], u[8];
-    mul32<true>(p, kkm + 32 * GP2, GP2, br, blk, warp, lane);
-    if (BACKWARD) mul32<false>(u, kkm + 32 * GP2, GP2, br, blk + 3 * nb, warp, lane);
+    {
+        const int o = warp * 16;
+        float* dst = lane < 16 ? tm : BACKWARD ? um : nullptr;
+        solve16(kkm + o * GP2 + o, br + o, dst ? dst + o * GP2 + o : nullptr, lane);
+        if (!(warp & 1) && dst)                                // right of it, above the diagonal
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        blk[2 * nb + (warp * 8 + r) * BP2 + lane] = p[r];
-        if (BACKWARD) blk[5 * nb + (warp * 8 + r) * BP2 + lane] = br[32 + warp * 8 + r] * u[r];
+            for (int i = 0; i < 16; ++i) dst[(o + i) * GP2 + o + 16 + (lane & 15)] = 0.f;
     }
     __syncthreads();
-#pragma unroll
-    for (int m = 0; m < (BACKWARD ? 2 : 1); ++m) {
-        const float* q = blk + 3 * nb * m;
-        mul32<false>(p, q + nb, BP2, br, q + 2 * nb, warp, lane);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int i = warp * 8 + r;
-            put_img(img, 32 + i, lane, -p[r]);
-            if (lane <= i) {
-                put_img(img, i, lane, q[i * BP2 + lane]);
-                put_img(img, 32 + i, 32 + lane, q[nb + i * BP2 + lane]);
-            }
-        }
+    if (warp < 2) join16<false>(kkm, br, tm, warp, lane);
+    if (BACKWARD && warp >= 2) join16<true>(kkm, br, um, warp - 2, lane);
+    __syncthreads();
+    join32<false>(kkm, br, tm, img, warp, lane);
+    __syncthreads();
+    copy_out(0);
+    if constexpr (BACKWARD) {
         __syncthreads();
-        copy_out(2 * m);
-        if (BACKWARD && m == 0) __syncthreads();
+        join32<true>(kkm, br, um, img, warp, lane);
+        __syncthreads();
+        copy_out(2);
     }
 }
 

@@ -7,28 +7,29 @@
 // chunk that starts from W solve (I + G diag(beta)) E = V - diag(gamma) K W^T.  So
 //   prep   (one warp per image, value head and chunk, all at once):
 //          T' = (I + G diag(beta))^{-1} by forward substitution, A = scale Gamma .* (Q K^T) for j <= i;
-//   chain  (one warp per 16 rows of W, sequential over the chunks):
+//   chain  (two warps per 16 rows of W, each with half of d_k, sequential over the chunks):
 //          R = V - diag(gamma) K W^T,  E = T' R,  U = diag(beta) E,
 //          Z = scale diag(gamma) Q W^T + A U,   W <- gamma_C W + U^T diag(Gamma_C.) K.
 // Every sum of log gates starts at zero (no difference of two long prefix sums), so a gate of -inf
 // (a state that is dropped) and strong gates keep their accuracy.
 //
-// The chain's rows are independent, so that a warp that owns 16 rows of W keeps them in registers as
+// The chain's rows are independent, so that two warps that own 16 rows of W keep them in registers as
 // the accumulators of U^T K, and each product's accumulators are the next one's left operand (the
-// m16n8k16 accumulator and A-operand layouts agree after a pack to bf16): W -> K W^T -> E -> W never
-// touches shared memory and no warp waits on another within a chunk.
+// m16n8k16 accumulator and A-operand layouts agree after a pack to bf16).  The two add up their halves of K W^T
+// through shared memory.  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
+// take the readout and the stores, one chunk behind.
 //
 // Precision: W is fp32.  As an operand it is split into P bf16 parts (2 for bf16 tokens: about 16
 // significant bits; 3 for fp32 tokens: about 24), as are R, E, U, T' and A; bf16 tokens are exact
 // operands, fp32 tokens are split into 3 parts by a pass of their own.  Products of parts below the last
 // kept part are dropped.
 //
-// Bound: the chain of chunks (per chunk and warp about 300 matrix instructions at d = 128, issued one per
-// 8 cycles per SM quarter: the instruction's rate here was measured at 1,009 multiply-adds per cycle and SM).
+// Bound: the chain of chunks, about 2,500 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
+// multiply-adds per cycle and SM, about half of it; the rest shared-memory reads of the token operands and the wait for
+// the other half).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 62 us, chain 346 us.
 #include <algorithm>
 #include <array>
 #include <atomic>
-#include <cstdlib>
 
 #include "delta.cuh"
 
@@ -156,8 +157,7 @@ __device__ __forceinline__ float row_dot(float init, const float* g, const float
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Row i, column `lane` of a bf16 part image.  (Rounded as a pair: the conversion of a single value runs at an eighth
-// of that rate and was what this kernel waited for.)
+// Row i, column `lane` of a bf16 part image.
 template <int P>
 __device__ __forceinline__ void put_part(uint8_t* mat, int i, int lane, float x) {
 #pragma unroll
@@ -272,8 +272,9 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
 // Chain
 // --------------------------------------------------------------------------------------------------
 // Two warps share a tile of 16 state rows and two helpers finish it.  With at most one tile per SM a CTA takes one
-// tile, else two, which share the token tiles in shared memory.
-static bool few_tiles(const Dims& d) { return (long long)d.B * d.h * (d.dv / 16) <= 148; }
+// tile, else two, which share the token tiles in shared memory.  2048 tokens, d = 128, forward by one / by two: 144 tiles
+// 98 / 107 us, 192 tiles 115 / 108; backward: 80 tiles 188 / 199, 256 tiles 398 / 337.
+static bool few_tiles(const Call& c) { return (long long)c.d.B * c.d.h * (c.d.dv / 16) <= c.sms; }
 
 struct ChainOut {
     View Z;                       // forward: the readout
@@ -997,14 +998,19 @@ static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, con
     return launch(k, grid, seq_warps<RT, KS>() * 32, spread_smem(L::smem, grid, c.sms), c.stream, a);
 }
 
-static bool use_tc(const Dims& d) { return d.dv == MV && !getenv("NOTC"); }
+// The tensor-memory chain gives a head one CTA, the register chain above gives it d_v / 32 (or d_v / 16), which finish
+// a chunk sooner but need more SMs: the former is chosen for d_v = 128 where the heads' states pass 32 x 128 values per SM.
+// bf16, d = 128, 2048 tokens, forward / backward, us, tensor memory against registers: 32 heads 128 / 344 against
+// 116 / 336; 40 heads 136 / 375 against 206 / 437; 148 heads 230 / 796 against 432 / 1256.  d_k = 64: 64 heads 134 / 400
+// against 132 / 466; 128 heads 176 / 579 against 253 / 832.
+static bool use_tc(const Call& c) { return c.d.dv == MV && (long long)c.d.B * c.d.h * MV * c.d.dk > 32LL * 128 * c.sms; }
 
 template <int DK, int P, int PK>
 static ttt_status forward_t(const Call& c) {
     const Layout l = layout(c.d, PK == 3, false);
     if constexpr (PK == 1) {
         TcArgs a{};
-        if (use_tc(c.d) && tc_args(&a, c, false, c.ws + l.rec) && tc_outputs(&a, c.Z, c.d, nullptr, 0, nullptr)) {
+        if (use_tc(c) && tc_args(&a, c, false, c.ws + l.rec) && tc_outputs(&a, c.Z, c.d, nullptr, 0, nullptr)) {
             a.W0 = c.W0;
             a.w0_bs = c.w0_bs;
             a.W1 = c.W1_out;
@@ -1020,7 +1026,7 @@ static ttt_status forward_t(const Call& c) {
     ChainOut out{};
     out.Z = c.Z;
     out.W1 = c.W1_out;
-    return few_tiles(c.d) ? run_chain_t<DK, P, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
+    return few_tiles(c) ? run_chain_t<DK, P, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
 }
 
 template <int DK, int P, int PK>
@@ -1048,7 +1054,7 @@ static ttt_status backward_t(const Call& c) {
     bool done = false;
     if constexpr (PK == 1) {
         TcArgs a{};
-        bool ok = use_tc(c.d) && tc_args(&a, c, true, rec);
+        bool ok = use_tc(c) && tc_args(&a, c, true, rec);
         TcArgs r = a;
         ok = ok && map64(&r.V, O, c.d, c.d.h, c.d.dv) && tc_outputs(&a, c.dV, c.d, out.E, ps, out.S) && tc_outputs(&r, c.dV, c.d, bo.Y, ps, bo.D);
         if (ok) {

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(128)
 delta_prep64(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, uint32_t* err) {
     using L = Prep64<DK, BACKWARD>;
     constexpr int KP = L::KP;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait_primary();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -293,8 +293,8 @@ ttt_status ttt_backward_mlp(const void* Q, const void* K, const void* V, const f
  *   G (log of the gate, normally <= 0; -inf drops the state), Beta: fp32, one value per token and value
  *   head (width 1).
  * Base pointers and strides of the token tensors are multiples of 16 bytes (strides of dimensions of
- * size 1 are ignored).  Inputs may be broadcast (stride 0) and may share memory; an output may share memory
- * with nothing else of the call.  Outputs cut from the rows of one buffer (equal token strides, columns
+ * size 1 are ignored).  Everything lies on the current device.  Inputs may be broadcast (stride 0) and may share
+ * memory; an output may share memory with nothing else of the call.  Outputs cut from the rows of one buffer (equal token strides, columns
  * that do not meet) are apart.
  *   lengths: NULL, or [batch] int32 on the device: sequence b has the first lengths[b] tokens (clamped to
  *   0 .. tokens).  What lies behind them is neither read nor written. */
@@ -310,14 +310,15 @@ typedef struct {
 
 /* Bytes of device workspace of ttt_forward_gated_delta (backward = 0) or ttt_backward_gated_delta
  * (backward = 1); 0 for an invalid shape.  It needs no zero fill; calls that may run at the same time
- * need distinct workspaces.  256-byte aligned. */
+ * need distinct workspaces.  256-byte aligned.  ttt_workspace_status tells whether a bounded wait of the last
+ * call on it ran out. */
 size_t ttt_gated_delta_workspace_bytes(int backward, const ttt_delta_shape* s);
 
 /* Whole sequences.  W0: NULL (zeros), [heads][d_v][d_k] fp32 shared by the batch (w0_shared = 1) or
  * [batch][heads][d_v][d_k] (w0_shared = 0).  W1_out: optional [batch][heads][d_v][d_k] fp32, the weights
  * after each sequence's last token.
- * Chunks of 32 tokens: inside a chunk the token updates are solved together (matrix products), the state goes
- * from chunk to chunk.  The state is fp32; bf16 tokens are exact operands and everything else is
+ * Chunks of 32 or 64 tokens: inside a chunk the token updates are solved together (matrix products), the state
+ * goes from chunk to chunk.  The state is fp32; bf16 tokens are exact operands and everything else is
  * carried as two bf16 parts (about 16 significant bits), fp32 tokens and everything else as three
  * (about 24).  Deterministic. */
 ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,

@@ -10,7 +10,7 @@ import torch
 import oracle
 from tests.parity import rel_max_err
 from tests.test_gated_delta_gpu import INPUTS, STATES, TOKENS, _check_backward, _check_forward, _lengths, _make, _on
-from vision_test_token_b200 import backward_gated_delta, forward_gated_delta
+from vision_test_token_b200 import backward_gated_delta, forward_gated_delta, step_gated_delta
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +147,16 @@ def test_same_bits_in_graphs_and_on_streams(cuda_dev):
         for got, ref in zip((captured, eager), want):
             for a, b in zip(got, ref):
                 assert torch.equal(a, b)
+
+
+def test_lengths_inside_an_output_are_refused(cuda_dev):
+    y = _on(_make(2, 1, 1, 40, 64, 64, seed=30), cuda_dev)
+    Z = torch.empty((2, 1, 40, 64), dtype=torch.bfloat16, device=cuda_dev)
+    lengths = Z.view(torch.int32).flatten()[:2]
+    lengths.fill_(40)
+    args = [y[n] for n in INPUTS]
+    with pytest.raises(RuntimeError, match="INVALID"):
+        forward_gated_delta(*args, lengths=lengths, Z=Z)
+    W = torch.zeros((2, 1, 64, 64), device=cuda_dev)
+    with pytest.raises(RuntimeError, match="INVALID"):
+        step_gated_delta(*args, W=W, slots=W.view(torch.int32).flatten()[:2])

@@ -13,13 +13,19 @@ ttt_status launch_clip(const void* const* in, void* const* out, const long long*
 
 namespace gd {
 
-static bool device_ptr(const void* p) {
+// Whether p is memory of the current device `dev`, or managed.
+static bool device_ptr(const void* p, int dev) {
     cudaPointerAttributes a;
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
         cudaGetLastError();   // clear the non-sticky error
         return false;
     }
-    return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
+    return (a.type == cudaMemoryTypeDevice && a.device == dev) || a.type == cudaMemoryTypeManaged;
+}
+static int current_device() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    return dev;
 }
 static bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
@@ -115,7 +121,7 @@ static ttt_status add_view(const ttt_view* v, int batch, int heads, int tokens, 
 // The views of a call: inputs may overlap one another and be broadcast (stride 0), outputs may overlap nothing.
 struct Checker {
     const ttt_delta_shape* s;
-    Slab slabs[16];
+    Slab slabs[16];               // a backward call's 11 views, W0, dW1, dW0, workspace and lengths
     bool output[16];
     int n = 0;
     ttt_status st = TTT_OK;
@@ -125,9 +131,9 @@ struct Checker {
         st = add_view(v, s->batch, heads, s->tokens, width, fp32 || s->dtype == TTT_FP32 ? 4 : 2, out, &slabs[n]);
         output[n++] = is_output;
     }
-    void flat(const void* p, long long bytes, bool is_output) {
+    void flat(const void* p, long long bytes, bool is_output, size_t align = 16) {
         if (st != TTT_OK || !p) return;
-        if (misaligned(p, 16)) { st = TTT_ERR_ALIGNMENT; return; }
+        if (misaligned(p, align)) { st = TTT_ERR_ALIGNMENT; return; }
         slabs[n] = Slab{static_cast<const char*>(p), {1, 1, 1}, {0, 0, 0}, 1, 1};
         slabs[n].n[0] = bytes;              // `bytes` single bytes in a row
         slabs[n].st[0] = 1;
@@ -140,8 +146,9 @@ struct Checker {
             for (int j = 0; j < i; ++j)
                 if ((output[i] || output[j]) && may_overlap(slabs[i], slabs[j])) return TTT_ERR_INVALID_ARG;
         }
+        const int dev = current_device();
         for (int i = 0; i < n; ++i)
-            if (!device_ptr(slabs[i].p)) return TTT_ERR_INVALID_ARG;
+            if (!device_ptr(slabs[i].p, dev)) return TTT_ERR_INVALID_ARG;
         return ttt_last_error();
     }
 };
@@ -151,12 +158,6 @@ static int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
     return n;
-}
-
-static ttt_status check_lengths(const int* lengths) {
-    if (!lengths) return TTT_OK;
-    if (misaligned(lengths, 4)) return TTT_ERR_ALIGNMENT;
-    return device_ptr(lengths) ? TTT_OK : TTT_ERR_INVALID_ARG;
 }
 
 }  // namespace gd
@@ -192,6 +193,7 @@ ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const t
     k.tokens(G, s->heads, 1, &c.G, false, true);
     k.tokens(Beta, s->heads, 1, &c.Beta, false, true);
     k.tokens(Z, s->heads, s->d_v, &c.Z, true);
+    k.flat(lengths, 4LL * s->batch, false, 4);
     k.flat(W0, w0_shared ? state : states, false);
     k.flat(W1_out, states, true);
     if (k.st != TTT_OK) return k.st;
@@ -200,7 +202,6 @@ ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const t
     if (misaligned(ws, 256)) return TTT_ERR_ALIGNMENT;
     k.flat(ws, (long long)need, true);
     st = k.finish();
-    if (st == TTT_OK) st = check_lengths(lengths);
     if (st != TTT_OK) return st;
     c.W0 = W0;
     c.w0_bs = w0_shared ? 0 : state / 4;
@@ -238,6 +239,7 @@ ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const 
     k.tokens(dV, s->heads, s->d_v, &c.dV, true);
     k.tokens(dG, s->heads, 1, &c.dG, true, true);
     k.tokens(dBeta, s->heads, 1, &c.dBeta, true, true);
+    k.flat(lengths, 4LL * s->batch, false, 4);
     k.flat(W0, w0_shared ? state : states, false);
     k.flat(dW1, states, false);
     k.flat(dW0_out, w0_shared ? state : states, true);
@@ -247,7 +249,6 @@ ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const 
     if (misaligned(ws, 256)) return TTT_ERR_ALIGNMENT;
     k.flat(ws, (long long)need, true);
     st = k.finish();
-    if (st == TTT_OK) st = check_lengths(lengths);
     if (st != TTT_OK) return st;
     c.W0 = W0;
     c.w0_bs = w0_shared ? 0 : state / 4;
@@ -279,9 +280,9 @@ ttt_status ttt_step_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_
     k.tokens(G, s->heads, 1, &c.G, false, true);
     k.tokens(Beta, s->heads, 1, &c.Beta, false, true);
     k.tokens(Z, s->heads, s->d_v, &c.Z, true);
+    k.flat(slots, 4LL * s->batch, false, 4);
     k.flat(W, (long long)n_slots * s->heads * s->d_v * s->d_k * 4, true);
     st = k.finish();
-    if (st == TTT_OK) st = check_lengths(slots);
     if (st != TTT_OK) return st;
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_step(c, W, slots, n_slots);
@@ -324,6 +325,7 @@ ttt_status ttt_clip_gradients(const void* const* grads, void* const* out, const 
         span(ws, (long long)clip_ws_bytes(n), n, true);
         span(norm_out, 4, n + 1, true);
         std::sort(spans, spans + m, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+        const int dev = current_device();
         const char *end_any = nullptr, *end_write = nullptr;    // furthest end seen, of any span and of an output
         for (int i = 0; i < m && st == TTT_OK; ++i) {
             if (spans[i].lo < (spans[i].write ? end_any : end_write)) st = TTT_ERR_INVALID_ARG;
@@ -331,7 +333,7 @@ ttt_status ttt_clip_gradients(const void* const* grads, void* const* out, const 
             if (spans[i].write) end_write = std::max(end_write, spans[i].hi);
         }
         for (int i = 0; i < m && st == TTT_OK; ++i)
-            if (!device_ptr(spans[i].lo)) st = TTT_ERR_INVALID_ARG;
+            if (!device_ptr(spans[i].lo, dev)) st = TTT_ERR_INVALID_ARG;
     }
     delete[] spans;
     if (st == TTT_OK) st = ttt_last_error();

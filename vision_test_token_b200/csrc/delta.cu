@@ -6,7 +6,7 @@
 // g_i) for j <= i and G_ij = Gamma_ij k_i.k_j for j < i, the residuals e_i = v_i - e^{g_i} W_{i-1} k_i of a
 // chunk that starts from W solve (I + G diag(beta)) E = V - diag(gamma) K W^T.  So
 //   prep   (one warp per image, value head and chunk, all at once):
-//          T' = (I + G diag(beta))^{-1} by forward substitution, A = scale Gamma .* (Q K^T) for j <= i;
+//          T' = (I + G diag(beta))^{-1}, A = scale Gamma .* (Q K^T) for j <= i;
 //   chain  (two warps per 16 rows of W, each with half of d_k, sequential over the chunks):
 //          R = V - diag(gamma) K W^T,  E = T' R,  U = diag(beta) E,
 //          Z = scale diag(gamma) Q W^T + A U,   W <- gamma_C W + U^T diag(Gamma_C.) K.
@@ -71,66 +71,65 @@ __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ Spli
 // --------------------------------------------------------------------------------------------------
 constexpr int GP = CT + 4;            // row pitch (floats) of the 32 x 32 fp32 matrices of a warp
 
-// Warps (chunks) per CTA: as many as leave room for a second CTA on the SM (bf16), or fit (fp32 parts).
-template <int DK, int PK>
-__host__ __device__ constexpr int prep_warps() { return PK == 1 ? 4 : 2; }
+// Warps (chunks) per CTA.
+constexpr int kPrepWarps = 4;
+// A warp's shared memory: Gamma, then G in its place, one matrix image, and two 16 x 16 blocks.
+template <int P>
+__host__ __device__ constexpr int prep_warp_bytes() { return CT * GP * 4 + mat_bytes(P) + 2 * 16 * 20 * 4; }
 
+// The lower triangles of K K^T (c) and Q K^T (w) of 32 tokens, rows behind `left` as zeros.  The operands go from global
+// memory to registers: any order of the features does as long as both sides have it, so that a lane takes 8
+// in a row, which are its operands of two products (each row of K being a left and a right operand).
 template <int DK, int PK>
-__host__ __device__ constexpr int prep_tile_bytes() { return PK * CT * (DK + 8) * 2; }
-// A warp's shared memory: the K and Q tiles, then, in their place, the two fp32 matrices and one matrix image.
-template <int DK, int P, int PK>
-__host__ __device__ constexpr int prep_warp_bytes() {
-    constexpr int tiles = 2 * prep_tile_bytes<DK, PK>(), after = 2 * CT * GP * 4 + mat_bytes(P);
-    return tiles > after ? tiles : after;
-}
-
-// 32 tokens x 32 tokens of X Y^T over DK features; X, Y [part][32][DK + 8].  Two 16-row tiles.
-template <int DK, int PK>
-__device__ __forceinline__ void gram32(float (&c)[2][4][4], uint32_t x, uint32_t y, int lane) {
-    constexpr int KP = DK + 8, PB = CT * KP * 2;
+__device__ __forceinline__ void gram32(float (&c)[2][4][4], float (&w)[2][4][4], const Parts& K, const Parts& Q, long long ko, long long qo,
+                                       int left, int lane) {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) c[m][n][q] = 0.f;
-    const int mi = lane >> 3, lr = lane & 7;
-    const uint32_t aoff = (((mi & 1) * 8 + lr) * KP + (mi >> 1) * 8) * 2;
-    const uint32_t boff = (((mi >> 1) * 8 + lr) * KP + (mi & 1) * 8) * 2;
-#pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) {
-        uint32_t b[PK][2][4];
+            for (int q = 0; q < 4; ++q) c[m][n][q] = w[m][n][q] = 0.f;
+#pragma unroll(PK == 1 ? 2 : 1)
+    for (int f = 0; f < DK; f += 32) {
+        uint4 k[PK][4], q[PK][4];
 #pragma unroll
         for (int p = 0; p < PK; ++p)
 #pragma unroll
-            for (int n2 = 0; n2 < 2; ++n2) ldsm4(b[p][n2], y + p * PB + boff + (n2 * 16 * KP + kk * 16) * 2);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-#pragma unroll
-            for (int pa = 0; pa < PK; ++pa) {
-                uint32_t a[4];
-                ldsm4(a, x + pa * PB + aoff + (m * 16 * KP + kk * 16) * 2);
-#pragma unroll
-                for (int pb = 0; pa + pb < PK; ++pb)
-#pragma unroll
-                    for (int n2 = 0; n2 <= m; ++n2) {        // the upper triangle is not used
-                        mma16816(c[m][2 * n2], a, b[pb][n2][0], b[pb][n2][1]);
-                        mma16816(c[m][2 * n2 + 1], a, b[pb][n2][2], b[pb][n2][3]);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const int row = g + 8 * i;
+                const bool live = row < left;
+                k[p][i] = live ? *reinterpret_cast<const uint4*>(K.p + p * K.ps + ko + row * K.ts + f + t * 8) : make_uint4(0, 0, 0, 0);
+                q[p][i] = live ? *reinterpret_cast<const uint4*>(Q.p + p * Q.ps + qo + row * Q.ts + f + t * 8) : make_uint4(0, 0, 0, 0);
             }
-        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int pa = 0; pa < PK; ++pa) {
+                    auto lo = [&](const uint4& v) { return half ? v.z : v.x; };
+                    auto hi = [&](const uint4& v) { return half ? v.w : v.y; };
+                    const uint32_t ak[4] = {lo(k[pa][2 * m]), lo(k[pa][2 * m + 1]), hi(k[pa][2 * m]), hi(k[pa][2 * m + 1])};
+                    const uint32_t aq[4] = {lo(q[pa][2 * m]), lo(q[pa][2 * m + 1]), hi(q[pa][2 * m]), hi(q[pa][2 * m + 1])};
+#pragma unroll
+                    for (int pb = 0; pa + pb < PK; ++pb)
+#pragma unroll
+                        for (int n = 0; n < 2 * m + 2; ++n) {
+                            mma16816(c[m][n], ak, lo(k[pb][n]), hi(k[pb][n]));
+                            mma16816(w[m][n], aq, lo(k[pb][n]), hi(k[pb][n]));
+                        }
+                }
     }
 }
 
-__device__ __forceinline__ void put32(float* dst, const float (&c)[2][4][4], int lane) {
-    const int g = lane >> 2, t = lane & 3;
+// Elements (i, j) and (i, j + 1), j even, of a bf16 part image.
+template <int P>
+__device__ __forceinline__ void put_parts2(uint8_t* mat, int i, int j, float x, float y) {
+    uint32_t w[P];
+    split2<P>(x, y, w);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            *reinterpret_cast<float2*>(dst + (m * 16 + g) * GP + n * 8 + 2 * t) = make_float2(c[m][n][0], c[m][n][1]);
-            *reinterpret_cast<float2*>(dst + (m * 16 + g + 8) * GP + n * 8 + 2 * t) = make_float2(c[m][n][2], c[m][n][3]);
-        }
+    for (int p = 0; p < P; ++p) *reinterpret_cast<uint32_t*>(mat + ((p * CT + i) * MP + j) * 2) = w[p];
 }
 
 // The warp's matrix image in shared memory -> global memory.
@@ -141,42 +140,109 @@ __device__ __forceinline__ void copy_image(uint8_t* dst, const uint8_t* image, i
     for (int x = lane; x < mat_bytes(P) / 16; x += 32) reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(image)[x];
     __syncwarp();
 }
-// init - g . y[0 .. i), g row i of a 32 x 32 fp32 matrix in shared memory (four sums at a time; i is a constant once
-// the caller's loop is unrolled).
-__device__ __forceinline__ float row_dot(float init, const float* g, const float (&y)[CT], int i) {
-    float s[4] = {init, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int l = 0; l < CT; l += 4) {
-        if (l >= i) continue;
-        const float4 v = *reinterpret_cast<const float4*>(g + l);
-        s[0] = fmaf(-v.x, y[l], s[0]);
-        if (l + 1 < i) s[1] = fmaf(-v.y, y[l + 1], s[1]);
-        if (l + 2 < i) s[2] = fmaf(-v.z, y[l + 2], s[2]);
-        if (l + 3 < i) s[3] = fmaf(-v.w, y[l + 3], s[3]);
-    }
-    return (s[0] + s[1]) + (s[2] + s[3]);
-}
+constexpr int XP = 20, kBlock = 16 * XP;   // row pitch and size (floats) of a 16 x 16 block
 
-// Row i, column `lane` of a bf16 part image.
-template <int P>
-__device__ __forceinline__ void put_part(uint8_t* mat, int i, int lane, float x) {
+// The image of (I + G diag(beta))^{-1} (U: of (I + diag(beta) G)^{-1}), G 32 x 32, strictly lower triangular.  The two 16 x 16
+// blocks on the diagonal are inverted by forward substitution, a column per lane; the block below them is
+// - T_22 L_21 T_11 on matrix instructions, whose operands are P parts as the image's elements are.
+template <int P, bool U>
+__device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, float* blocks, float beta, int lane) {
+    {
+        const int half = lane >> 4, col = lane & 15;
+        const float* gh = gm + half * 16 * (GP + 1);
+        float y[16];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const uint32_t w = pack2(x, 0.f);
-        reinterpret_cast<uint16_t*>(mat)[(p * CT + i) * MP + lane] = (uint16_t)w;
-        x -= lo_f(w);
+        for (int i = 0; i < 16; ++i) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int l = 0; l < 16; l += 4) {
+                if (l >= i) continue;
+                const float4 v = *reinterpret_cast<const float4*>(gh + i * GP + l);
+                s[0] = fmaf(v.x, y[l], s[0]);
+                if (l + 1 < i) s[1] = fmaf(v.y, y[l + 1], s[1]);
+                if (l + 2 < i) s[2] = fmaf(v.z, y[l + 2], s[2]);
+                if (l + 3 < i) s[3] = fmaf(v.w, y[l + 3], s[3]);
+            }
+            const float be = __shfl_sync(~0u, beta, half * 16 + i), sum = (s[0] + s[1]) + (s[2] + s[3]);
+            const float x = i < col ? 0.f : (i == col ? 1.f : 0.f) - (U ? be * sum : sum);
+            blocks[half * kBlock + i * XP + col] = x;
+            y[i] = U ? x : be * x;
+        }
+    }
+    __syncwarp();
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t m[P][4];                              // T_22 L_21, its accumulators as the next left operand
+    {
+        uint32_t a[P][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = *reinterpret_cast<const float2*>(blocks + kBlock + (g + (e & 1) * 8) * XP + 2 * t + (e >> 1) * 8);
+            uint32_t w[P];
+            split2<P>(v.x, v.y, w);
+#pragma unroll
+            for (int p = 0; p < P; ++p) a[p][e] = w[p];
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t b[P][2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int k = 16 + 2 * t + e * 8;
+                const float f0 = __shfl_sync(~0u, beta, U ? k : n * 8 + g), f1 = __shfl_sync(~0u, beta, U ? k + 1 : n * 8 + g);
+                uint32_t w[P];
+                split2<P>(f0 * gm[k * GP + n * 8 + g], f1 * gm[(k + 1) * GP + n * 8 + g], w);
+#pragma unroll
+                for (int p = 0; p < P; ++p) b[p][e] = w[p];
+            }
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int pa = 0; pa < P; ++pa)
+#pragma unroll
+                for (int pb = 0; pa + pb < P; ++pb) mma16816(c, a[pa], b[pb][0], b[pb][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t w[P];
+                split2<P>(c[2 * e], c[2 * e + 1], w);
+#pragma unroll
+                for (int p = 0; p < P; ++p) m[p][2 * n + e] = w[p];
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        uint32_t b[P][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float* x = blocks + (2 * t + e * 8) * XP + n * 8 + g;
+            uint32_t w[P];
+            split2<P>(x[0], x[XP], w);
+#pragma unroll
+            for (int p = 0; p < P; ++p) b[p][e] = w[p];
+        }
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int pa = 0; pa < P; ++pa)
+#pragma unroll
+            for (int pb = 0; pa + pb < P; ++pb) mma16816(c, m[pa], b[pb][0], b[pb][1]);
+        put_parts2<P>(image, 16 + g, n * 8 + 2 * t, -c[0], -c[1]);
+        put_parts2<P>(image, 24 + g, n * 8 + 2 * t, -c[2], -c[3]);
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const int block = r >> 2, i = (r & 3) * 4 + (lane >> 3), j = (lane & 7) * 2;
+        const float2 v = *reinterpret_cast<const float2*>(blocks + block * kBlock + i * XP + j);
+        put_parts2<P>(image, block * 16 + i, block * 16 + j, v.x, v.y);
     }
 }
 
 template <int DK, int P, int PK, bool BACKWARD>
-__global__ void __launch_bounds__(prep_warps<DK, PK>() * 32)
+__global__ void __launch_bounds__(kPrepWarps * 32, PK == 1 ? 4 : 2)
 delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long total, uint32_t* err) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int KP = DK + 8;
     pdl_launch_dependents();
     pdl_wait_primary();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long item = (long long)blockIdx.x * prep_warps<DK, PK>() + warp;
+    const long long item = (long long)blockIdx.x * kPrepWarps + warp;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0;
     if (item >= total) return;
     const int c = (int)(item % d.nc);
@@ -184,27 +250,10 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
     const int h = (int)(bh % d.h), b = (int)(bh / d.h);
     const int left = seq_len(d, b) - c * CT;
     if (left <= 0) return;
-    uint8_t* my = smem + warp * prep_warp_bytes<DK, P, PK>();
-    const uint32_t kt = s32(my), qt = kt + prep_tile_bytes<DK, PK>();
+    uint8_t* my = smem + warp * prep_warp_bytes<P>();
     float* kkm = reinterpret_cast<float*>(my);
-    float* qkm = kkm + CT * GP;
-    uint8_t* image = my + 2 * CT * GP * 4;
-    {
-        const long long ko = b * K.bs + (h / d.r) * K.hs + (long long)c * CT * K.ts;
-        const long long qo = b * Q.bs + (h / d.r) * Q.hs + (long long)c * CT * Q.ts;
-        constexpr int CPR = DK / 8;
-#pragma unroll
-        for (int p = 0; p < PK; ++p)
-#pragma unroll 4
-            for (int x = lane; x < CT * CPR; x += 32) {
-                const int row = x / CPR, col = x % CPR;
-                const bool live = row < left;
-                const long long rk = live ? row : 0;
-                cp16(kt + (p * CT * KP + row * KP + col * 8) * 2, K.p + p * K.ps + ko + rk * K.ts + col * 8, live);
-                cp16(qt + (p * CT * KP + row * KP + col * 8) * 2, Q.p + p * Q.ps + qo + rk * Q.ts + col * 8, live);
-            }
-        cp_commit();
-    }
+    uint8_t* image = my + CT * GP * 4;
+    float* blocks = reinterpret_cast<float*>(image + mat_bytes(P));
     // gates of token `lane`; tokens past the end of the sequence neither fade nor write
     const long long t = (long long)c * CT + lane;
     const bool live = lane < left;
@@ -224,46 +273,47 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
     gates[CT + lane] = expf(suf);
     gates[2 * CT + lane] = beta;
 
-    cp_wait<0>();
-    __syncwarp();
     {
-        float m[2][4][4], w[2][4][4];
-        gram32<DK, PK>(m, kt, kt, lane);
-        gram32<DK, PK>(w, qt, kt, lane);
-        __syncwarp();                                  // the tiles have been read: the matrices take their place
-        put32(kkm, m, lane);
-        put32(qkm, w, lane);
-    }
-    __syncwarp();
-    // column `lane` (= j): Gamma_ij with its log summed from zero at i = j
-    uint8_t* Tm = out + kGateBytes;
-    float s = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < CT; ++i) {
-        const float gi = __shfl_sync(~0u, g, i);
-        s = i > lane ? s + gi : 0.f;
-        // bf16 tokens: the fast exponential, relative error about 2^-22 (1 + |s|)
-        const float dec = i < lane ? 0.f : PK == 1 ? __expf(s) : expf(s);
-        put_part<P>(image, i, lane, i >= lane ? d.scale * dec * qkm[i * GP + lane] : 0.f);
-        kkm[i * GP + lane] = i > lane ? dec * kkm[i * GP + lane] : 0.f;
-    }
-    copy_image<P>(Tm + mat_bytes(P), image, lane);
-    // forward substitution, one column per lane
-    float y[CT];
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-        const float x = row_dot(i == lane ? 1.f : 0.f, kkm + i * GP, y, i);
-        put_part<P>(image, i, lane, x);
-        y[i] = x * __shfl_sync(~0u, beta, i);
-    }
-    copy_image<P>(Tm, image, lane);
-    if constexpr (BACKWARD) {
+        // column `lane` (= j): Gamma_ij with its log summed from zero at i = j
+        float s = 0.f;
 #pragma unroll
         for (int i = 0; i < CT; ++i) {
-            const float x = (i == lane ? 1.f : 0.f) + __shfl_sync(~0u, beta, i) * row_dot(0.f, kkm + i * GP, y, i);
-            put_part<P>(image, i, lane, x);
-            y[i] = x;
+            const float gi = __shfl_sync(~0u, g, i);
+            s = i > lane ? s + gi : 0.f;
+            // bf16 tokens: the fast exponential, relative error about 2^-22 (1 + |s|)
+            kkm[i * GP + lane] = i < lane ? 0.f : PK == 1 ? __expf(s) : expf(s);
         }
+    }
+    __syncwarp();
+    uint8_t* Tm = out + kGateBytes;
+    {
+        float m[2][4][4], w[2][4][4];
+        gram32<DK, PK>(m, w, K, Q, b * K.bs + (h / d.r) * K.hs + (long long)c * CT * K.ts, b * Q.bs + (h / d.r) * Q.hs + (long long)c * CT * Q.ts,
+                       left, lane);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = x * 16 + (lane >> 2) + e * 8, j = n * 8 + 2 * (lane & 3);
+                    if (n > 2 * x + 1) {                       // above the diagonal (G is zero there already)
+                        put_parts2<P>(image, i, j, 0.f, 0.f);
+                        continue;
+                    }
+                    const bool edge = n >= 2 * x;              // the diagonal may pass: nothing above it may come through, NaN neither
+                    float2* dec = reinterpret_cast<float2*>(kkm + i * GP + j);
+                    const float2 gm = *dec;
+                    put_parts2<P>(image, i, j, edge && j > i ? 0.f : d.scale * gm.x * w[x][n][2 * e],
+                                  edge && j + 1 > i ? 0.f : d.scale * gm.y * w[x][n][2 * e + 1]);
+                    *dec = make_float2(edge && j >= i ? 0.f : gm.x * m[x][n][2 * e], edge && j + 1 >= i ? 0.f : gm.y * m[x][n][2 * e + 1]);
+                }
+    }
+    copy_image<P>(Tm + mat_bytes(P), image, lane);
+    inverse_image<P, false>(image, kkm, blocks, beta, lane);   // what lies above the diagonal is zero from A on
+    copy_image<P>(Tm, image, lane);
+    if constexpr (BACKWARD) {
+        inverse_image<P, true>(image, kkm, blocks, beta, lane);
         copy_image<P>(Tm + 2 * mat_bytes(P), image, lane);
     }
 }
@@ -976,7 +1026,7 @@ struct Splitter {
 
 template <int DK, int P, int PK, bool BACKWARD>
 static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_t* rec) {
-    constexpr int kPrepWarps = prep_warps<DK, PK>(), smem = kPrepWarps * prep_warp_bytes<DK, P, PK>();
+    constexpr int smem = kPrepWarps * prep_warp_bytes<P>();
     constexpr auto k = delta_prep<DK, P, PK, BACKWARD>;
     ttt_status st = allow_smem<k>(smem);
     if (st != TTT_OK) return st;

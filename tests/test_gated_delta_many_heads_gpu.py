@@ -160,3 +160,25 @@ def test_lengths_inside_an_output_are_refused(cuda_dev):
     W = torch.zeros((2, 1, 64, 64), device=cuda_dev)
     with pytest.raises(RuntimeError, match="INVALID"):
         step_gated_delta(*args, W=W, slots=W.view(torch.int32).flatten()[:2])
+
+
+@pytest.mark.parametrize("h", [2, 20])
+def test_images_far_apart(cuda_dev, h):
+    """Images more than 2^31 elements apart in one buffer: the same bits as side by side."""
+    B, N, d = 2, 70, 128
+    y = _on(_make(B, h, h, N, d, d, layout="tokens", w0="shared", seed=11), cuda_dev)
+    far = 2 ** 31 + 2 ** 10
+    buf = torch.zeros(far + 8 * N * h * d, dtype=torch.bfloat16, device=cuda_dev)
+    cut = lambda i: torch.as_strided(buf, (B, h, N, d), (far, d, 8 * h * d, 1), i * h * d)  # noqa: E731
+    z = dict(y)
+    for i, n in enumerate(("Q", "K", "V", "dZ")):
+        z[n] = cut(i)
+        z[n].copy_(y[n])
+    Z = forward_gated_delta(*(y[n] for n in INPUTS), W0=y["W0"])
+    forward_gated_delta(*(z[n] for n in INPUTS), W0=y["W0"], Z=cut(4))
+    assert torch.equal(cut(4), Z)
+    want = backward_gated_delta(*(y[n] for n in INPUTS), y["dZ"], W0=y["W0"], dW1=y["dW1"])
+    got = [cut(5), cut(6), cut(7)] + [torch.empty_like(t) for t in want[3:]]
+    backward_gated_delta(*(z[n] for n in INPUTS), z["dZ"], W0=y["W0"], dW1=y["dW1"], out=got)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -56,11 +56,8 @@ struct Slab {
     const char* p;
     long long n[3], st[3];        // batch, heads, tokens
     int width, esz;
-    long long span() const {      // bytes from the first to past the last element
-        long long e = width;
-        for (int i = 0; i < 3; ++i) e += (n[i] - 1) * st[i];
-        return e * esz;
-    }
+    long long image() const { return ((n[1] - 1) * st[1] + (n[2] - 1) * st[2] + width) * esz; }   // bytes from the first to past the last
+    long long span() const { return image() + (n[0] - 1) * st[0] * esz; }
 };
 
 // Whether two elements of the slab may share an address: its dimensions, ordered by stride, have to nest.
@@ -89,11 +86,14 @@ static bool may_overlap(const Slab& a, const Slab& b) {
             row = r;
         }
     if (row == 0) return true;
+    // equal batch strides that keep the images apart: image b of one can only meet image b of the other
+    const long long apart = (b.p > a.p ? b.p - a.p : a.p - b.p) + std::max(a.image(), b.image());
+    const bool by_image = a.n[0] == b.n[0] && a.st[0] == b.st[0] && apart <= a.st[0] * a.esz;
     long long lo[2], hi[2];
     const Slab* s[2] = {&a, &b};
     for (int i = 0; i < 2; ++i) {
         const bool whole_rows = s[i]->n[0] == 1 || (s[i]->st[0] * s[i]->esz) % row == 0;
-        if (!whole_rows) return true;
+        if (!whole_rows && !by_image) return true;
         const long long w = ((s[i]->n[1] - 1) * s[i]->st[1] + s[i]->width) * s[i]->esz;
         if (w > row) return true;
         lo[i] = i == 0 ? 0 : ((b.p - a.p) % row + row) % row;

@@ -26,7 +26,7 @@
 //
 // Bound: the chain of chunks, about 2,500 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
 // multiply-adds per cycle and SM, about half of it; the rest shared-memory reads of the token operands and the wait for
-// the other half).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 62 us, chain 346 us.
+// the other half).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep about 50 us, chain 350 us.
 #include <algorithm>
 #include <array>
 #include <atomic>
@@ -71,7 +71,9 @@ __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ Spli
 // --------------------------------------------------------------------------------------------------
 constexpr int GP = CT + 4;            // row pitch (floats) of the 32 x 32 fp32 matrices of a warp
 
-// Warps (chunks) per CTA.
+// Warps (chunks) per CTA.  Bound: issue and latency of about 2,000 instructions per warp (sixteen warps per SM) with 3 TB/s of
+// reads and records beside them.  Four CTAs per SM at 128 registers and two groups of 32 features in flight took 401 us
+// for the forward call above, five with one group 400, six with one 411.
 constexpr int kPrepWarps = 4;
 // A warp's shared memory: Gamma, then G in its place, one matrix image, and two 16 x 16 blocks.
 template <int P>

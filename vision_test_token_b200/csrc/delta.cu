@@ -7,26 +7,28 @@
 // chunk that starts from W solve (I + G diag(beta)) E = V - diag(gamma) K W^T.  So
 //   prep   (one warp per image, value head and chunk, all at once):
 //          T' = (I + G diag(beta))^{-1}, A = scale Gamma .* (Q K^T) for j <= i;
-//   chain  (two warps per 16 rows of W, each with half of d_k, sequential over the chunks):
+//   chain  (a warp per 16 rows of W, sequential over the chunks):
 //          R = V - diag(gamma) K W^T,  E = T' R,  U = diag(beta) E,
 //          Z = scale diag(gamma) Q W^T + A U,   W <- gamma_C W + U^T diag(Gamma_C.) K.
 // Every sum of log gates starts at zero (no difference of two long prefix sums), so a gate of -inf
 // (a state that is dropped) and strong gates keep their accuracy.
 //
-// The chain's rows are independent, so that two warps that own 16 rows of W keep them in registers as
+// The chain's rows are independent, so that a warp that owns 16 rows of W keeps them in registers as
 // the accumulators of U^T K, and each product's accumulators are the next one's left operand (the
-// m16n8k16 accumulator and A-operand layouts agree after a pack to bf16).  The two add up their halves of K W^T
-// through shared memory.  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
-// take the readout and the stores, one chunk behind.
+// m16n8k16 accumulator and A-operand layouts agree after a pack to bf16): W -> K W^T -> E -> W never waits on another
+// warp within a chunk.  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
+// take the readout and the stores, one chunk behind.  In the backward pass, whose helpers have more to do, two warps share
+// 16 rows, each with half of d_k, and add up their halves of K W^T through shared memory (KS = 2).  One warp against two:
+// forward, 32 heads of 8192 tokens, d = 128, 366 us against 400; backward, 32 heads of 4096, 672 us against 594.
 //
 // Precision: W is fp32.  As an operand it is split into P bf16 parts (2 for bf16 tokens: about 16
 // significant bits; 3 for fp32 tokens: about 24), as are R, E, U, T' and A; bf16 tokens are exact
 // operands, fp32 tokens are split into 3 parts by a pass of their own.  Products of parts below the last
 // kept part are dropped.
 //
-// Bound: the chain of chunks, about 2,500 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
-// multiply-adds per cycle and SM, about half of it; the rest shared-memory reads of the token operands and the wait for
-// the other half).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep about 50 us, chain 350 us.
+// Bound: the chain of chunks, about 2,250 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
+// multiply-adds per cycle and SM, about half of it; the rest is their latency and shared-memory reads of the token
+// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep about 50 us, chain 315 us.
 #include <algorithm>
 #include <array>
 #include <atomic>
@@ -73,7 +75,7 @@ constexpr int GP = CT + 4;            // row pitch (floats) of the 32 x 32 fp32 
 
 // Warps (chunks) per CTA.  Bound: issue and latency of about 2,000 instructions per warp (sixteen warps per SM) with 3 TB/s of
 // reads and records beside them.  Four CTAs per SM at 128 registers and two groups of 32 features in flight took 401 us
-// for the forward call above, five with one group 400, six with one 411.
+// for the forward call above (with the chain of that time), five with one group 400, six with one 411.
 constexpr int kPrepWarps = 4;
 // A warp's shared memory: Gamma, then G in its place, one matrix image, and two 16 x 16 blocks.
 template <int P>
@@ -323,9 +325,9 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
 // --------------------------------------------------------------------------------------------------
 // Chain
 // --------------------------------------------------------------------------------------------------
-// Two warps share a tile of 16 state rows and two helpers finish it.  With at most one tile per SM a CTA takes one
+// A tile is 16 state rows, and two helpers finish it.  With at most one tile per SM a CTA takes one
 // tile, else two, which share the token tiles in shared memory.  2048 tokens, d = 128, forward by one / by two: 144 tiles
-// 98 / 107 us, 192 tiles 115 / 108; backward: 80 tiles 188 / 199, 256 tiles 398 / 337.
+// 90 / 98 us, 192 tiles 106 / 99; backward: 80 tiles 188 / 199, 256 tiles 398 / 337.
 static bool few_tiles(const Call& c) { return (long long)c.d.B * c.d.h * (c.d.dv / 16) <= c.sms; }
 
 struct ChainOut {
@@ -1053,8 +1055,9 @@ static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, con
 // The tensor-memory chain gives a head one CTA, the register chain above gives it d_v / 32 (or d_v / 16), which finish
 // a chunk sooner but need more SMs: the former is chosen for d_v = 128 where the heads' states pass 32 x 128 values per SM.
 // bf16, d = 128, 2048 tokens, forward / backward, us, tensor memory against registers: 32 heads 128 / 344 against
-// 116 / 336; 40 heads 136 / 375 against 206 / 437; 148 heads 230 / 796 against 432 / 1256.  d_k = 64: 64 heads 134 / 400
-// against 132 / 466; 128 heads 176 / 579 against 253 / 832.
+// 102 / 336; 40 heads 137 / 375 against 186 / 437; 148 heads 230 / 796 against 388 / 1256.  d_k = 64: 64 heads 134 / 400
+// against 129 / 466; 128 heads 178 / 579 against 250 / 832.  (Just above the limit, sequences of under 64 tokens lose up
+// to a quarter by it: 40 heads of 16 tokens 25 / 55 against 20 / 47.)
 static bool use_tc(const Call& c) { return c.d.dv == MV && (long long)c.d.B * c.d.h * MV * c.d.dk > 32LL * 128 * c.sms; }
 
 template <int DK, int P, int PK>
@@ -1078,7 +1081,7 @@ static ttt_status forward_t(const Call& c) {
     ChainOut out{};
     out.Z = c.Z;
     out.W1 = c.W1_out;
-    return few_tiles(c) ? run_chain_t<DK, P, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
+    return few_tiles(c) ? run_chain_t<DK, P, PK, 1, 1>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 1>(c, Q, K, c.ws + l.rec, out);
 }
 
 template <int DK, int P, int PK>

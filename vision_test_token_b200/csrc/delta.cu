@@ -708,11 +708,14 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             }
         };
         for (int c = 0; c < L::kStages - 1; ++c) issue(c);
+        int good = nch + 1;                           // periods before the first whose loads did not come in time
         for (int c = 0; c <= nch; ++c) {
-            if (loads_in(c)) mbar_wait(&ctl.full[c % L::kStages], (c / L::kStages) & 1, ab);
+            if (c < good && loads_in(c) && !__all_sync(~0u, mbar_wait(&ctl.full[c % L::kStages], (c / L::kStages) & 1, ab))) good = c;
             __syncthreads();
-            issue(c + L::kStages - 1);
+            if (c < good) issue(c + L::kStages - 1);
         }
+        for (int c = good; c <= nch && c < good + L::kStages - 1; ++c)       // nothing may still be on its way when the CTA ends
+            if (loads_in(c)) mbar_drain(&ctl.full[c % L::kStages], (c / L::kStages) & 1, ab.limit);
         return;
     }
     if (warp >= CW) {

@@ -109,11 +109,15 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             }
         };
         for (int k = -1; k < L::kStages - 2; ++k) issue(k);
+        int good = nch + 1;                           // periods before the first whose loads did not come in time
         for (int k = -1; k <= nch; ++k) {
-            if (k < nch && nch > 0) mbar_wait(&ctl.full[(k + 1) % L::kStages], ((k + 1) / L::kStages) & 1, ab);
+            if (k < good && k < nch && nch > 0 && !__all_sync(~0u, mbar_wait(&ctl.full[(k + 1) % L::kStages], ((k + 1) / L::kStages) & 1, ab)))
+                good = k;
             __syncthreads();
-            issue(k + L::kStages - 1);
+            if (k < good) issue(k + L::kStages - 1);
         }
+        for (int k = good; k < nch && k < good + L::kStages - 1; ++k)        // nothing may still be on its way when the CTA ends
+            mbar_drain(&ctl.full[(k + 1) % L::kStages], ((k + 1) / L::kStages) & 1, ab.limit);
         return;
     }
     if (warp >= CW) {

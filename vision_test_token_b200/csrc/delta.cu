@@ -715,7 +715,7 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             if (c < good) issue(c + L::kStages - 1);
         }
         for (int c = good; c <= nch && c < good + L::kStages - 1; ++c)       // nothing may still be on its way when the CTA ends
-            if (loads_in(c)) mbar_drain(&ctl.full[c % L::kStages], (c / L::kStages) & 1, ab.limit);
+            if (loads_in(c)) mbar_drain(&ctl.full[c % L::kStages], (c / L::kStages) & 1, drain_limit(ab));
         return;
     }
     if (warp >= CW) {

@@ -96,6 +96,10 @@ __device__ __forceinline__ void stsm4t(uint32_t a, uint32_t r0, uint32_t r1, uin
                  "r"(r3)
                  : "memory");
 }
+// How long a CTA that gives up waits for its own copies and products: 50 ms at least, however short the call's limit, since what
+// lands after its end lands in another CTA's memory.
+__device__ __forceinline__ unsigned long long drain_limit(const Abort& ab) { return max(ab.limit, 50000000ull); }
+
 // D (16 x 8, fp32) += A (16 x 16, bf16) * B (16 x 8, bf16).
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"

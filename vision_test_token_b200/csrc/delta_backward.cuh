@@ -117,7 +117,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             if (k < good) issue(k + L::kStages - 1);
         }
         for (int k = good; k < nch && k < good + L::kStages - 1; ++k)        // nothing may still be on its way when the CTA ends
-            mbar_drain(&ctl.full[(k + 1) % L::kStages], ((k + 1) / L::kStages) & 1, ab.limit);
+            mbar_drain(&ctl.full[(k + 1) % L::kStages], ((k + 1) / L::kStages) & 1, drain_limit(ab));
         return;
     }
     if (warp >= CW) {

@@ -169,10 +169,9 @@ delta_grads_tc(const __grid_constant__ GradsArgs p) {
                     }
                 }
             }
-            if (!ok) {                             // nothing may still be on its way when the CTA ends
-                if (kq > 0) mbar_drain(&ctl.kq_full, (kq - 1) & 1, ab.limit);
-                for (uint32_t k = sl > 2 ? sl - 2 : 0; k < sl; ++k) mbar_drain(&ctl.full[k & 1], (k >> 1) & 1, ab.limit);
-            }
+            // nothing may still be on its way when the CTA ends
+            if (kq > 0) mbar_drain(&ctl.kq_full, (kq - 1) & 1, drain_limit(ab));
+            for (uint32_t k = sl > 2 ? sl - 2 : 0; k < sl; ++k) mbar_drain(&ctl.full[k & 1], (k >> 1) & 1, drain_limit(ab));
         }
     } else if (warp == 9) {
         // ---------------------------------------------------------------- products
@@ -244,9 +243,9 @@ delta_grads_tc(const __grid_constant__ GradsArgs p) {
         if (!ok) {
             if (elect_one()) mma_commit(&ctl.fin);
             __syncwarp();
-            mbar_drain(&ctl.fin, n & 1, ab.limit);
+            mbar_drain(&ctl.fin, n & 1, drain_limit(ab));
         } else if (n > 0) {
-            mbar_drain(&ctl.fin, (n - 1) & 1, ab.limit);
+            mbar_drain(&ctl.fin, (n - 1) & 1, drain_limit(ab));
         }
     } else if (warp >= 10) {
         // ---------------------------------------------------------------- gates, Gamma and <D, W>

@@ -577,14 +577,12 @@ __device__ __forceinline__ void chain_tc_body(const TcArgs& p, int bh) {
     if (warp == 12) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
-        for (int c = 0; c < nch; ++c) {
+        int c = 0;
+        for (; c < nch; ++c) {
             const int s = c % L::kStages, left = len - c * TC;
             if (c >= L::kStages) ok = mbar_wait(&ctl.empty[s], (c / L::kStages - 1) & 1, ab);
             ok = __all_sync(~0u, ok);
-            if (!ok) {                             // nothing may still be on its way when the CTA ends
-                for (int k = max(0, c - L::kStages); k < c; ++k) mbar_drain(&ctl.full[k % L::kStages], (k / L::kStages) & 1, ab.limit);
-                break;
-            }
+            if (!ok) break;
             const uint32_t st = sb + s * L::stage;
             if (left < TC) {
                 tok64_tail<DK>(st + L::oK, p.K, b, h / d.r, c * TC, left, lane);
@@ -605,6 +603,8 @@ __device__ __forceinline__ void chain_tc_body(const TcArgs& p, int bh) {
             }
             __syncwarp();
         }
+        // nothing may still be on its way when the CTA ends
+        for (int i = max(0, c - L::kStages); i < c; ++i) mbar_drain(&ctl.full[i % L::kStages], (i / L::kStages) & 1, drain_limit(ab));
     } else if (warp == 13) {
         // ---------------------------------------------------------------- products
         constexpr uint32_t id64 = idesc_bf16_f32(MV, 64, false, false), idS = idesc_bf16_f32(MV, DK, false, true);
@@ -688,9 +688,9 @@ __device__ __forceinline__ void chain_tc_body(const TcArgs& p, int bh) {
         if (!ok) {
             if (elect_one()) mma_commit(&ctl.sd);
             __syncwarp();
-            mbar_drain(&ctl.sd, c & 1, ab.limit);
+            mbar_drain(&ctl.sd, c & 1, drain_limit(ab));
         } else if (nch > 0) {
-            mbar_drain(SAVE ? &ctl.sd : &ctl.z2, (nch - 1) & 1, ab.limit);
+            mbar_drain(SAVE ? &ctl.sd : &ctl.z2, (nch - 1) & 1, drain_limit(ab));
         }
     } else {
         // rows of the state: tensor-memory lane <-> row of this thread
@@ -933,14 +933,12 @@ __device__ __forceinline__ void reverse_tc_body(const TcArgs& p, int bh) {
     if (warp == 12) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
-        for (int k = 0; k < nch; ++k) {
+        int k = 0;
+        for (; k < nch; ++k) {
             const int s = k % L::kStages, c = nch - 1 - k, left = len - c * TC;
             if (k >= L::kStages) ok = mbar_wait(&ctl.empty[s], (k / L::kStages - 1) & 1, ab);
             ok = __all_sync(~0u, ok);
-            if (!ok) {                             // nothing may still be on its way when the CTA ends
-                for (int n = max(0, k - L::kStages); n < k; ++n) mbar_drain(&ctl.full[n % L::kStages], (n / L::kStages) & 1, ab.limit);
-                break;
-            }
+            if (!ok) break;
             const uint32_t st = sb + s * L::stage;
             if (left < TC) {
                 tok64_tail<DK>(st + L::oK, p.K, b, h / d.r, c * TC, left, lane);
@@ -962,6 +960,7 @@ __device__ __forceinline__ void reverse_tc_body(const TcArgs& p, int bh) {
             }
             __syncwarp();
         }
+        for (int i = max(0, k - L::kStages); i < k; ++i) mbar_drain(&ctl.full[i % L::kStages], (i / L::kStages) & 1, drain_limit(ab));
     } else if (warp == 13) {
         // ---------------------------------------------------------------- products
         constexpr uint32_t id64 = idesc_bf16_f32(MV, 64, false, false), idS = idesc_bf16_f32(MV, DK, false, true);
@@ -1040,9 +1039,9 @@ __device__ __forceinline__ void reverse_tc_body(const TcArgs& p, int bh) {
         if (!ok) {
             if (elect_one()) mma_commit(&ctl.sd);
             __syncwarp();
-            mbar_drain(&ctl.sd, k & 1, ab.limit);
+            mbar_drain(&ctl.sd, k & 1, drain_limit(ab));
         } else if (nch > 0) {
-            mbar_drain(&ctl.sd, (nch - 1) & 1, ab.limit);
+            mbar_drain(&ctl.sd, (nch - 1) & 1, drain_limit(ab));
         }
     } else {
         const int q = warp & 3;

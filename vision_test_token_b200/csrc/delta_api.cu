@@ -119,7 +119,7 @@ static ttt_status add_view(const ttt_view* v, int batch, int heads, int tokens, 
 }
 
 // The views of a call: inputs may overlap one another and be broadcast (stride 0), outputs may overlap nothing.
-struct Checker {
+struct Arguments {
     const ttt_delta_shape* s;
     Slab slabs[16];               // a backward call's 11 views, W0, dW1, dW0, workspace and lengths
     bool output[16];
@@ -186,7 +186,7 @@ ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const t
     c.d.lengths = lengths;
     c.d.scale = scale;
     const long long state = (long long)s->heads * s->d_v * s->d_k * 4, states = state * s->batch;
-    Checker k{s};
+    Arguments k{s};
     k.tokens(Q, s->qk_heads, s->d_k, &c.Q, false);
     k.tokens(K, s->qk_heads, s->d_k, &c.K, false);
     k.tokens(V, s->heads, s->d_v, &c.V, false);
@@ -227,7 +227,7 @@ ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const 
     c.d.lengths = lengths;
     c.d.scale = scale;
     const long long state = (long long)s->heads * s->d_v * s->d_k * 4, states = state * s->batch;
-    Checker k{s};
+    Arguments k{s};
     k.tokens(Q, s->qk_heads, s->d_k, &c.Q, false);
     k.tokens(K, s->qk_heads, s->d_k, &c.K, false);
     k.tokens(V, s->heads, s->d_v, &c.V, false);
@@ -273,7 +273,7 @@ ttt_status ttt_step_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_
     c.d = dims_of(*s);
     c.fp32 = s->dtype == TTT_FP32;
     c.d.scale = scale;
-    Checker k{s};
+    Arguments k{s};
     k.tokens(Q, s->qk_heads, s->d_k, &c.Q, false);
     k.tokens(K, s->qk_heads, s->d_k, &c.K, false);
     k.tokens(V, s->heads, s->d_v, &c.V, false);

@@ -317,10 +317,10 @@ size_t ttt_gated_delta_workspace_bytes(int backward, const ttt_delta_shape* s);
 /* Whole sequences.  W0: NULL (zeros), [heads][d_v][d_k] fp32 shared by the batch (w0_shared = 1) or
  * [batch][heads][d_v][d_k] (w0_shared = 0).  W1_out: optional [batch][heads][d_v][d_k] fp32, the weights
  * after each sequence's last token.
- * Chunks of 32 or 64 tokens: inside a chunk the token updates are solved together (matrix products), the state
- * goes from chunk to chunk.  The state is fp32; bf16 tokens are exact operands and everything else is
- * carried as two bf16 parts (about 16 significant bits), fp32 tokens and everything else as three
- * (about 24).  Deterministic. */
+ * Chunks of 32 tokens: inside a chunk the token updates are solved together (matrix products), the state
+ * goes from chunk to chunk.  The state and all sums are fp32.  As operands of matrix instructions, bf16 tokens are exact and
+ * everything else is carried as three bf16 parts (24 significant bits); but what ends in bf16 outputs alone (Z, dQ and dK of bf16
+ * tokens) may be carried as two (16 bits).  Deterministic. */
 ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,
                                    const ttt_view* Beta, const float* W0, int w0_shared, const int* lengths, float scale,
                                    const ttt_view* Z, float* W1_out, const ttt_delta_shape* s, void* ws, size_t ws_bytes,

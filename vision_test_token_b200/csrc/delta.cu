@@ -16,19 +16,22 @@
 // The chain's rows are independent, so that a warp that owns 16 rows of W keeps them in registers as
 // the accumulators of U^T K, and each product's accumulators are the next one's left operand (the
 // m16n8k16 accumulator and A-operand layouts agree after a pack to bf16): W -> K W^T -> E -> W never waits on another
-// warp within a chunk.  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
-// take the readout and the stores, one chunk behind.  In the backward pass, whose helpers have more to do, two warps share
-// 16 rows, each with half of d_k, and add up their halves of K W^T through shared memory (KS = 2).  One warp against two:
-// forward, 32 heads of 8192 tokens, d = 128, 366 us against 400; backward, 32 heads of 4096, 672 us against 594.
+// warp within a chunk, but for one: two warps share 16 rows, each with half of d_k, and add up their halves of K W^T through
+// shared memory (KS = 2).  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
+// take the readout and the stores, one chunk behind.  One warp for 16 rows against two: forward, 32 heads of 8192 tokens, d = 128,
+// 566 us against 439, 48 heads of 6084, d = 64, 288 against 285; backward, 32 heads of 4096, d = 128, 1190 against 1105.
 //
-// Precision: W is fp32.  As an operand it is split into P bf16 parts (2 for bf16 tokens: about 16
-// significant bits; 3 for fp32 tokens: about 24), as are R, E, U, T' and A; bf16 tokens are exact
-// operands, fp32 tokens are split into 3 parts by a pass of their own.  Products of parts below the last
-// kept part are dropped.
+// Precision: W and all sums are fp32.  An operand of a matrix instruction that no bf16 value holds is split into bf16 parts,
+// products of parts below the last kept one dropped: PF = 3 parts (24 bits) wherever an fp32 result comes from it (W, R, T', suffix U; for fp32
+// tokens, themselves split by a pass of their own, all of them), two in the readout of bf16 tokens (W, U, A), whose Z is rounded to
+// eight bits anyway.  The matrix instructions truncate: each of an instruction's products is cut at a quarter of the last place of the
+// largest addend, and the sum towards zero.  So sums of many products are taken in accumulators of their own, the small
+// products first or apart, and added to the rest in fp32.  2-norm errors, d = 64 .. 128, gates of 0 .. -3: W1 1 to 2e-7, fp32 Z 2e-7, gradients in fp32
+// 1 to 5e-7; a plain fp32 computation in chunks: 1 to 4e-7.  (Two parts for R and suffix U alone: W1 2.4e-6 and 2.6e-6.)
 //
-// Bound: the chain of chunks, about 2,250 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
+// Bound: the chain of chunks, about 2,950 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
 // multiply-adds per cycle and SM, about half of it; the rest is their latency and shared-memory reads of the token
-// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep about 50 us, chain 315 us.
+// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 52 us, chain 385 us.
 #include <algorithm>
 #include <array>
 #include <atomic>
@@ -73,13 +76,11 @@ __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ Spli
 // --------------------------------------------------------------------------------------------------
 constexpr int GP = CT + 4;            // row pitch (floats) of the 32 x 32 fp32 matrices of a warp
 
-// Warps (chunks) per CTA.  Bound: issue and latency of about 2,000 instructions per warp (sixteen warps per SM) with 3 TB/s of
-// reads and records beside them.  Four CTAs per SM at 128 registers and two groups of 32 features in flight took 401 us
-// for the forward call above (with the chain of that time), five with one group 400, six with one 411.
+// Warps (chunks) per CTA.  Bound: issue and latency of about 2,000 instructions per warp with 3 TB/s of reads and records beside them.
+// Shared memory (59 KB a CTA) keeps three CTAs, twelve warps, on an SM.
 constexpr int kPrepWarps = 4;
 // A warp's shared memory: Gamma, then G in its place, one matrix image, and two 16 x 16 blocks.
-template <int P>
-__host__ __device__ constexpr int prep_warp_bytes() { return CT * GP * 4 + mat_bytes(P) + 2 * 16 * 20 * 4; }
+constexpr int kPrepWarpBytes = CT * GP * 4 + mat_bytes(PF) + 2 * 16 * 20 * 4;
 
 // The lower triangles of K K^T (c) and Q K^T (w) of 32 tokens, rows behind `left` as zeros.  The operands go from global
 // memory to registers: any order of the features does as long as both sides have it, so that a lane takes 8
@@ -106,24 +107,35 @@ __device__ __forceinline__ void gram32(float (&c)[2][4][4], float (&w)[2][4][4],
                 k[p][i] = live ? *reinterpret_cast<const uint4*>(K.p + p * K.ps + ko + row * K.ts + f + t * 8) : make_uint4(0, 0, 0, 0);
                 q[p][i] = live ? *reinterpret_cast<const uint4*>(Q.p + p * Q.ps + qo + row * Q.ts + f + t * 8) : make_uint4(0, 0, 0, 0);
             }
+        // more than one part: the products of a block are summed in accumulators of their own, the small ones first
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int n = 0; n < 2 * m + 2; ++n) {
+                float uc[4] = {}, uw[4] = {};
 #pragma unroll
-                for (int pa = 0; pa < PK; ++pa) {
-                    auto lo = [&](const uint4& v) { return half ? v.z : v.x; };
-                    auto hi = [&](const uint4& v) { return half ? v.w : v.y; };
-                    const uint32_t ak[4] = {lo(k[pa][2 * m]), lo(k[pa][2 * m + 1]), hi(k[pa][2 * m]), hi(k[pa][2 * m + 1])};
-                    const uint32_t aq[4] = {lo(q[pa][2 * m]), lo(q[pa][2 * m + 1]), hi(q[pa][2 * m]), hi(q[pa][2 * m + 1])};
+                for (int order = PK - 1; order >= 0; --order)
 #pragma unroll
-                    for (int pb = 0; pa + pb < PK; ++pb)
+                    for (int pb = 0; pb < PK; ++pb) {
+                        const int pa = order - pb;
+                        if (pa < 0) continue;
 #pragma unroll
-                        for (int n = 0; n < 2 * m + 2; ++n) {
-                            mma16816(c[m][n], ak, lo(k[pb][n]), hi(k[pb][n]));
-                            mma16816(w[m][n], aq, lo(k[pb][n]), hi(k[pb][n]));
+                        for (int half = 0; half < 2; ++half) {
+                            auto lo = [&](const uint4& v) { return half ? v.z : v.x; };
+                            auto hi = [&](const uint4& v) { return half ? v.w : v.y; };
+                            const uint32_t ak[4] = {lo(k[pa][2 * m]), lo(k[pa][2 * m + 1]), hi(k[pa][2 * m]), hi(k[pa][2 * m + 1])};
+                            const uint32_t aq[4] = {lo(q[pa][2 * m]), lo(q[pa][2 * m + 1]), hi(q[pa][2 * m]), hi(q[pa][2 * m + 1])};
+                            mma16816(PK > 1 ? uc : c[m][n], ak, lo(k[pb][n]), hi(k[pb][n]));
+                            mma16816(PK > 1 ? uw : w[m][n], aq, lo(k[pb][n]), hi(k[pb][n]));
                         }
-                }
+                    }
+                if (PK > 1)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        c[m][n][e] += uc[e];
+                        w[m][n][e] += uw[e];
+                    }
+            }
     }
 }
 
@@ -143,6 +155,11 @@ __device__ __forceinline__ void copy_image(uint8_t* dst, const uint8_t* image, i
 #pragma unroll
     for (int x = lane; x < mat_bytes(P) / 16; x += 32) reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(image)[x];
     __syncwarp();
+}
+// Zeros in the 16 x 16 block above the diagonal blocks of an image's last part.
+template <int P>
+__device__ __forceinline__ void zero_upper(uint8_t* image, int lane) {
+    *reinterpret_cast<uint4*>(image + (((P - 1) * CT + (lane >> 1)) * MP + 16 + (lane & 1) * 8) * 2) = make_uint4(0, 0, 0, 0);
 }
 constexpr int XP = 20, kBlock = 16 * XP;   // row pitch and size (floats) of a 16 x 16 block
 
@@ -240,7 +257,7 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
 }
 
 template <int DK, int P, int PK, bool BACKWARD>
-__global__ void __launch_bounds__(kPrepWarps * 32, PK == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kPrepWarps * 32, PK == 1 ? 3 : 2)
 delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long total, uint32_t* err) {
     extern __shared__ __align__(16) uint8_t smem[];
     pdl_launch_dependents();
@@ -254,10 +271,10 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
     const int h = (int)(bh % d.h), b = (int)(bh / d.h);
     const int left = seq_len(d, b) - c * CT;
     if (left <= 0) return;
-    uint8_t* my = smem + warp * prep_warp_bytes<P>();
+    uint8_t* my = smem + warp * kPrepWarpBytes;
     float* kkm = reinterpret_cast<float*>(my);
     uint8_t* image = my + CT * GP * 4;
-    float* blocks = reinterpret_cast<float*>(image + mat_bytes(P));
+    float* blocks = reinterpret_cast<float*>(image + mat_bytes(PF));
     // gates of token `lane`; tokens past the end of the sequence neither fade nor write
     const long long t = (long long)c * CT + lane;
     const bool live = lane < left;
@@ -284,12 +301,10 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
         for (int i = 0; i < CT; ++i) {
             const float gi = __shfl_sync(~0u, g, i);
             s = i > lane ? s + gi : 0.f;
-            // bf16 tokens: the fast exponential, relative error about 2^-22 (1 + |s|)
-            kkm[i * GP + lane] = i < lane ? 0.f : PK == 1 ? __expf(s) : expf(s);
+            kkm[i * GP + lane] = i < lane ? 0.f : expf(s);
         }
     }
     __syncwarp();
-    uint8_t* Tm = out + kGateBytes;
     {
         float m[2][4][4], w[2][4][4];
         gram32<DK, PK>(m, w, K, Q, b * K.bs + (h / d.r) * K.hs + (long long)c * CT * K.ts, b * Q.bs + (h / d.r) * Q.hs + (long long)c * CT * Q.ts,
@@ -313,12 +328,13 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
                     *dec = make_float2(edge && j >= i ? 0.f : gm.x * m[x][n][2 * e], edge && j + 1 >= i ? 0.f : gm.y * m[x][n][2 * e + 1]);
                 }
     }
-    copy_image<P>(Tm + mat_bytes(P), image, lane);
-    inverse_image<P, false>(image, kkm, blocks, beta, lane);   // what lies above the diagonal is zero from A on
-    copy_image<P>(Tm, image, lane);
+    copy_image<P>(out + kRecA, image, lane);
+    if (P < PF) zero_upper<PF>(image, lane);
+    inverse_image<PF, false>(image, kkm, blocks, beta, lane);  // what lies above the diagonal is zero from A on
+    copy_image<PF>(out + kGateBytes, image, lane);
     if constexpr (BACKWARD) {
-        inverse_image<P, true>(image, kkm, blocks, beta, lane);
-        copy_image<P>(Tm + 2 * mat_bytes(P), image, lane);
+        inverse_image<PF, true>(image, kkm, blocks, beta, lane);
+        copy_image<PF>(out + kRecA + mat_bytes(P), image, lane);
     }
 }
 
@@ -327,7 +343,7 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
 // --------------------------------------------------------------------------------------------------
 // A tile is 16 state rows, and two helpers finish it.  With at most one tile per SM a CTA takes one
 // tile, else two, which share the token tiles in shared memory.  2048 tokens, d = 128, forward by one / by two: 144 tiles
-// 90 / 98 us, 192 tiles 106 / 99; backward: 80 tiles 188 / 199, 256 tiles 398 / 337.
+// 101 / 110 us, 192 tiles 190 / 111; backward: 80 tiles 299 / 303, 256 tiles 669 / 572.
 static bool few_tiles(const Call& c) { return (long long)c.d.B * c.d.h * (c.d.dv / 16) <= c.sms; }
 
 struct ChainOut {
@@ -361,8 +377,8 @@ struct ChainLayout {
     static constexpr int kK = PK * CT * DK * 2;                // K of the period's chunk, then Q of the one before
     static constexpr int kQ = SAVE ? 0 : kK;
     static constexpr int kV = CT * VB;
-    static constexpr int kM = mat_bytes(P);                    // T', then A of the chunk before
-    static constexpr int stage = (kK + kQ + kV + (SAVE ? 1 : 2) * kM + 1023) / 1024 * 1024;
+    static constexpr int kT = mat_bytes(PF), kA = SAVE ? 0 : mat_bytes(P);     // T', then A of the chunk before
+    static constexpr int stage = (kK + kQ + kV + kT + kA + 1023) / 1024 * 1024;
     static constexpr int kGates = kGateSlots * kGateBytes;
     static constexpr int kS = DK / 16 * P * 512;               // a tile's state as operand parts
     static constexpr int kE = 2048;                            // a tile's residuals (or partial sums), fp32
@@ -375,22 +391,27 @@ struct ChainLayout {
 };
 
 // acc (16 x 8) += (parts a of 16 rows x 32 k) * B for one block nb of 8 columns, B a lower-triangular matrix image
-// [32][MP].  NT: B[k][n] = M[n][k] (columns n of the product are M's rows);  else B[k][n] = M[k][n].
-template <int P, int PA, bool NT>
+// [PM parts][32][MP]; the products of the smallest parts first.  NT: B[k][n] = M[n][k] (columns n of the product are M's
+// rows);  else B[k][n] = M[k][n].
+template <int PM, int PA, bool NT>
 __device__ __forceinline__ void mat_block(float (&acc)[4], const uint32_t (&a)[2][PA][4], uint32_t mat, int nb, int lane) {
+    constexpr int P = PM > PA ? PM : PA;
     const int mi = lane >> 3, lr = lane & 7;
+    uint32_t b[PM][4];
 #pragma unroll
-    for (int pb = 0; pb < P; ++pb) {
-        uint32_t b[4];
-        if (NT) ldsm4(b, mat + ((pb * CT + nb * 8 + lr) * MP + mi * 8) * 2);
-        else ldsm4t(b, mat + ((pb * CT + mi * 8 + lr) * MP + nb * 8) * 2);
-#pragma unroll
-        for (int pa = 0; pa < PA; ++pa)
-            if (pa + pb < P) {
-                if (NT || nb < 2) mma16816(acc, a[0][pa], b[0], b[1]);
-                if (!NT || nb >= 2) mma16816(acc, a[1][pa], b[2], b[3]);
-            }
+    for (int pb = 0; pb < PM; ++pb) {
+        if (NT) ldsm4(b[pb], mat + ((pb * CT + nb * 8 + lr) * MP + mi * 8) * 2);
+        else ldsm4t(b[pb], mat + ((pb * CT + mi * 8 + lr) * MP + nb * 8) * 2);
     }
+#pragma unroll
+    for (int order = P - 1; order >= 0; --order)
+#pragma unroll
+        for (int pb = 0; pb < PM; ++pb) {
+            const int pa = order - pb;
+            if (pa < 0 || pa >= PA) continue;
+            if (NT || nb < 2) mma16816(acc, a[0][pa], b[pb][0], b[pb][1]);
+            if (!NT || nb >= 2) mma16816(acc, a[1][pa], b[pb][2], b[pb][3]);
+        }
 }
 
 // The parts of accumulator blocks (2 kk, 2 kk + 1) as a left operand for k block kk.
@@ -416,30 +437,45 @@ __device__ __forceinline__ void as_operand(uint32_t (&a)[P][4], const float (&x)
 template <int DK>
 constexpr int kTilePart = CT * DK * 2;
 
-// s (16 x DW columns from col0) += (parts a: 16 x 16 tokens of block kk) * X, X a token tile.
+// s (16 x DW columns from col0) = fade s + (parts a: 16 x 32 tokens) * X, X a token tile.  Each block's products are
+// summed in accumulators of their own, the small ones first, and added to s in fp32.
 template <int DK, int DW, int P, int PK>
-__device__ __forceinline__ void add_outer(float (&s)[DW / 8][4], const uint32_t (&a)[P][4], uint32_t x, int kk, int col0, int lane) {
+__device__ __forceinline__ void fade_add_outer(float (&s)[DW / 8][4], float fade, const uint32_t (&a)[2][P][4], uint32_t x, int col0, int lane) {
     const int mi = lane >> 3, lr = lane & 7;
     const int c16 = col0 / 16;                     // first 16-column block: DW / 16 blocks, aligned to their number
-    const uint32_t base = x + (kk * 16 + (mi & 1) * 8 + lr) * 128 + ((((mi >> 1) ^ lr) << 4) ^ ((c16 & 3) << 5)) + (c16 >> 2) * 4096;
+    const uint32_t base = x + ((mi & 1) * 8 + lr) * 128 + ((((mi >> 1) ^ lr) << 4) ^ ((c16 & 3) << 5)) + (c16 >> 2) * 4096;
 #pragma unroll
-    for (int n2 = 0; n2 < DW / 16; ++n2)
+    for (int n2 = 0; n2 < DW / 16; ++n2) {
+        uint32_t b[2][PK][4];
 #pragma unroll
-        for (int pb = 0; pb < PK; ++pb) {
-            uint32_t b[4];
-            ldsm4t(b, (base ^ ((n2 & 3) << 5)) + (n2 >> 2) * 4096 + pb * kTilePart<DK>);
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int pa = 0; pa + pb < P; ++pa) {
-                mma16816(s[2 * n2], a[pa], b[0], b[1]);
-                mma16816(s[2 * n2 + 1], a[pa], b[2], b[3]);
+            for (int pb = 0; pb < PK; ++pb) ldsm4t(b[kk][pb], (base ^ ((n2 & 3) << 5)) + (n2 >> 2) * 4096 + kk * 2048 + pb * kTilePart<DK>);
+        float u[2][2][4] = {};
+#pragma unroll
+        for (int order = P - 1; order >= 0; --order)
+#pragma unroll
+            for (int pb = 0; pb < PK; ++pb) {
+                if (pb > order) continue;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    mma16816(u[kk][0], a[kk][order - pb], b[kk][pb][0], b[kk][pb][1]);
+                    mma16816(u[kk][1], a[kk][order - pb], b[kk][pb][2], b[kk][pb][3]);
+                }
             }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            s[2 * n2][q] = fmaf(fade, s[2 * n2][q], u[0][0][q] + u[1][0][q]);
+            s[2 * n2 + 1][q] = fmaf(fade, s[2 * n2 + 1][q], u[0][1][q] + u[1][1][q]);
         }
+    }
 }
 
-// acc (16 x 16 tokens, from token 16 n2) += (parts a: 16 x 16 features from col) * X^T, X a token tile.
+// acc (16 x 16 tokens, from token 16 n2) += (parts a: 16 x 16 features from col) * X^T, X a token tile: the products of the
+// first parts to acc, the others to low.
 template <int DK, int P, int PK>
-__device__ __forceinline__ void dot_tokens(float (&acc0)[4], float (&acc1)[4], const uint32_t (&a)[P][4], uint32_t x, int n2, int c16,
-                                           int lane) {
+__device__ __forceinline__ void dot_tokens(float (&acc0)[4], float (&acc1)[4], float (&low0)[4], float (&low1)[4], const uint32_t (&a)[P][4],
+                                           uint32_t x, int n2, int c16, int lane) {
     const int mi = lane >> 3, lr = lane & 7;
     const uint32_t base = x + (n2 * 16 + (mi >> 1) * 8 + lr) * 128 + ((((mi & 1) ^ lr) << 4) ^ ((c16 & 3) << 5)) + (c16 >> 2) * 4096;
 #pragma unroll
@@ -448,8 +484,8 @@ __device__ __forceinline__ void dot_tokens(float (&acc0)[4], float (&acc1)[4], c
         ldsm4(b, base + pb * kTilePart<DK>);
 #pragma unroll
         for (int pa = 0; pa + pb < P; ++pa) {
-            mma16816(acc0, a[pa], b[0], b[1]);
-            mma16816(acc1, a[pa], b[2], b[3]);
+            mma16816(pa + pb ? low0 : acc0, a[pa], b[0], b[1]);
+            mma16816(pa + pb ? low1 : acc1, a[pa], b[2], b[3]);
         }
     }
 }
@@ -691,8 +727,8 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             if (lane == 0) {
                 fence_proxy_async_smem();             // the warp's own stores to the stage, before the copies' writes
                 uint32_t n = 0;
-                if (now) n += Loader::bytes(K, left, L::kK) + Loader::bytes(V, left, L::kV) + kGateBytes + L::kM;
-                if (before) n += Loader::bytes(Q, left + CT, L::kK) + L::kM;
+                if (now) n += Loader::bytes(K, left, L::kK) + Loader::bytes(V, left, L::kV) + kGateBytes + L::kT;
+                if (before) n += Loader::bytes(Q, left + CT, L::kK) + L::kA;
                 mbar_arrive_expect_tx(l.bar, n);
             }
             __syncwarp();
@@ -700,11 +736,11 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                 load_tokens<DK, PK>(l, st, K, b, h / d.r, c * CT, left);
                 l.template tile<L::VB, PK == 1 ? 2 : 4>(st + L::kK + L::kQ, V, 0, b, h, c * CT, v0, left);
                 l.flat(gate_slot(c), r, kGateBytes);
-                l.flat(st + L::kK + L::kQ + L::kV, r + kGateBytes, L::kM);
+                l.flat(st + L::kK + L::kQ + L::kV, r + kGateBytes, L::kT);
             }
             if (before) {
                 load_tokens<DK, PK>(l, st + L::kK, Q, b, h / d.r, c * CT - CT, left + CT);
-                l.flat(st + L::kK + L::kQ + L::kV + L::kM, r - recb + kGateBytes + L::kM, L::kM);
+                l.flat(st + L::kK + L::kQ + L::kV + L::kT, r - recb + kRecA, L::kA);
             }
         };
         for (int c = 0; c < L::kStages - 1; ++c) issue(c);
@@ -736,8 +772,8 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                     put_state_parts<DK, P>(sp, out.S + ((long long)bh * d.ng + (pc * CT) / d.gt) * P * state, d.dv, row0, z, lane);
             } else {
                 // Z of tokens [16 z, 16 z + 16) = scale gamma (Q W^T) + A U
-                const uint32_t st = stage_of(c), qt = st + L::kK, am = st + L::kK + L::kQ + L::kV + L::kM;
-                float acc[2][4] = {};
+                const uint32_t st = stage_of(c), qt = st + L::kK, am = st + L::kK + L::kQ + L::kV + L::kT;
+                float acc[2][4] = {}, low[2][4] = {};
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk) {
                     uint32_t a[P][4];
@@ -746,7 +782,7 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                         const uint4 v = lds4u(sp + ((kk * P + p) * 32 + lane) * 16);
                         a[p][0] = v.x; a[p][1] = v.y; a[p][2] = v.z; a[p][3] = v.w;
                     }
-                    dot_tokens<DK, P, PK>(acc[0], acc[1], a, qt, z, kk, lane);
+                    dot_tokens<DK, P, PK>(acc[0], acc[1], low[0], low[1], a, qt, z, kk, lane);
                 }
                 uint32_t u[2][P][4];
 #pragma unroll
@@ -764,8 +800,10 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                 for (int i = 0; i < 2; ++i) {
                     const int nb = 2 * z + i;
                     const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
-                    acc[i][0] *= d.scale * ga.x; acc[i][1] *= d.scale * ga.y; acc[i][2] *= d.scale * ga.x; acc[i][3] *= d.scale * ga.y;
-                    mat_block<P, P, true>(acc[i], u, am, nb, lane);
+                    float au[4] = {};
+                    mat_block<P, P, true>(au, u, am, nb, lane);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(d.scale * ((q & 1) ? ga.y : ga.x), acc[i][q] + low[i][q], au[q]);
                 }
                 put_pair_tokens<PK>(stagebuf, acc[0], acc[1], out.Z.p,
                                     b * out.Z.bs + h * out.Z.hs + ((long long)pc * CT + z * 16) * out.Z.ts + row0, out.Z.ts, left - z * 16, lane);
@@ -785,18 +823,23 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
         const uint32_t sp = sbuf + ((c & 1) * RT + rt) * L::kS, ep = ebuf + ((c & 1) * RT + rt) * L::kE;
         const bool hand = !SAVE || (c * CT) % d.gt == 0;
 
-        float x[4][4] = {};
+        float x[4][4] = {}, low[4][4] = {};
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
-            uint32_t a[P][4];
-            as_operand<P>(a, s[2 * kk], s[2 * kk + 1]);
+            uint32_t a[PF][4];
+            as_operand<PF>(a, s[2 * kk], s[2 * kk + 1]);
 #pragma unroll
-            for (int n2 = 0; n2 < 2; ++n2) dot_tokens<DK, P, PK>(x[2 * n2], x[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
+            for (int n2 = 0; n2 < 2; ++n2)
+                dot_tokens<DK, PF, PK>(x[2 * n2], x[2 * n2 + 1], low[2 * n2], low[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
             if (hand) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) sts4u(sp + (((ks * KB + kk) * P + p) * 32 + lane) * 16, a[p]);
             }
         }
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[nb][q] += low[nb][q];
         if constexpr (KS > 1) {
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) sts4(xp + ((ks * 4 + nb) * 32 + lane) * 16, x[nb]);
@@ -834,17 +877,12 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
         }
         // E = T' R
         float e[4][4] = {};
-        uint32_t a[2][P][4];
-        as_operand<P>(a[0], x[0], x[1]);
-        as_operand<P>(a[1], x[2], x[3]);
+        uint32_t a[2][PF][4];
+        as_operand<PF>(a[0], x[0], x[1]);
+        as_operand<PF>(a[1], x[2], x[3]);
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) mat_block<P, P, true>(e[nb], a, tm, nb, lane);
+        for (int nb = 0; nb < 4; ++nb) mat_block<PF, PF, true>(e[nb], a, tm, nb, lane);
         // W <- gamma_C W + (suffix beta E)^T K
-        const float gc = lds1(gt + (CT - 1) * 4);
-#pragma unroll
-        for (int nb = 0; nb < DW / 8; ++nb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) s[nb][q] *= gc;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
             if (nb / NBW == ks) sts4(ep + (nb * 32 + lane) * 16, e[nb]);
@@ -852,11 +890,9 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             const float u0 = su.x * be.x, u1 = su.y * be.y;
             e[nb][0] *= u0; e[nb][1] *= u1; e[nb][2] *= u0; e[nb][3] *= u1;
         }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            as_operand<P>(a[kk], e[2 * kk], e[2 * kk + 1]);
-            add_outer<DK, DW, P, PK>(s, a[kk], kt, kk, col0, lane);
-        }
+        as_operand<PF>(a[0], e[0], e[1]);
+        as_operand<PF>(a[1], e[2], e[3]);
+        fade_add_outer<DK, DW, PF, PK>(s, lds1(gt + (CT - 1) * 4), a, kt, col0, lane);
     }
     if (out.W1) put_state<DK, DW>(s, out.W1 + (long long)bh * state, row0, col0, lane);
 }
@@ -904,12 +940,6 @@ static bool encode_map(CUtensorMap* m, const void* p, int esz, std::array<cuuint
                rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// A plain [rows][cols] bf16 matrix with boxes of 64 columns x `rows_box` rows.
-static bool encode_map2(CUtensorMap* m, const void* p, int cols, long long rows, int rows_box) {
-    const long long all = rows * cols;
-    return encode_map(m, p, 2, {(cuuint64_t)cols, (cuuint64_t)rows, 1, 1, 1}, {cols, all, all, all}, 128, rows_box);
-}
-
 // The map of a [part][batch][heads][tokens][width] tensor with boxes of 32 tokens x rb bytes.
 static Tiled tiled(const void* p, long long ps, int parts, long long bs, long long hs, long long ts, const Dims& d, int heads, int width,
                    int esz, int rb) {
@@ -965,7 +995,6 @@ static ttt_status allow_smem(int bytes) {
 
 static uint32_t* error_word(const Call& c) { return reinterpret_cast<uint32_t*>(c.ws); }
 
-#include "delta_tc.cuh"
 #include "delta_backward.cuh"
 
 // --------------------------------------------------------------------------------------------------
@@ -975,13 +1004,12 @@ struct Layout {
     size_t rec, qp, kp, op, E, Y, S, D, dw, part, total;
 };
 static Layout layout(const Dims& d, bool fp32, bool backward) {
-    const int P = fp32 ? 3 : 2;
+    const int P = fp32 || backward ? PF : 2;
     Layout l{};
     size_t at = kWsHeader;
     auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
     const size_t heads = (size_t)d.B * d.h, toks = heads * d.N;
-    const size_t rec = heads * d.nc * rec_bytes(P, backward);
-    l.rec = take(fp32 ? rec : std::max(rec, heads * ((d.N + TC - 1) / TC) * tc_rec_bytes(backward)));
+    l.rec = take(heads * d.nc * rec_bytes(P, backward));
     if (fp32) {
         l.qp = take((size_t)3 * d.B * d.hk * d.N * d.dk * 2);
         l.kp = take((size_t)3 * d.B * d.hk * d.N * d.dk * 2);
@@ -993,7 +1021,7 @@ static Layout layout(const Dims& d, bool fp32, bool backward) {
         l.S = take(heads * d.ng * P * d.dv * d.dk * 2);
         l.D = take(heads * d.ng * P * d.dv * d.dk * 2);
         l.dw = take(heads * d.dv * d.dk * 4);
-        if (!fp32 && d.r > 1) l.part = take(2 * toks * d.dk * 4);
+        if (d.r > 1) l.part = take(2 * toks * d.dk * 4);
     }
     l.total = at;
     return l;
@@ -1033,7 +1061,7 @@ struct Splitter {
 
 template <int DK, int P, int PK, bool BACKWARD>
 static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_t* rec) {
-    constexpr int smem = kPrepWarps * prep_warp_bytes<P>();
+    constexpr int smem = kPrepWarps * kPrepWarpBytes;
     constexpr auto k = delta_prep<DK, P, PK, BACKWARD>;
     ttt_status st = allow_smem<k>(smem);
     if (st != TTT_OK) return st;
@@ -1055,27 +1083,9 @@ static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, con
     return launch(k, grid, seq_warps<RT, KS>() * 32, spread_smem(L::smem, grid, c.sms), c.stream, a);
 }
 
-// The tensor-memory chain gives a head one CTA, the register chain above gives it d_v / 32 (or d_v / 16), which finish
-// a chunk sooner but need more SMs: the former is chosen for d_v = 128 where the heads' states pass 32 x 128 values per SM.
-// bf16, d = 128, 2048 tokens, forward / backward, us, tensor memory against registers: 32 heads 128 / 344 against
-// 102 / 336; 40 heads 137 / 375 against 186 / 437; 148 heads 230 / 796 against 388 / 1256.  d_k = 64: 64 heads 134 / 400
-// against 129 / 466; 128 heads 178 / 579 against 250 / 832.  (Just above the limit, sequences of under 64 tokens lose up
-// to a quarter by it: 40 heads of 16 tokens 25 / 55 against 20 / 47.)
-static bool use_tc(const Call& c) { return c.d.dv == MV && (long long)c.d.B * c.d.h * MV * c.d.dk > 32LL * 128 * c.sms; }
-
 template <int DK, int P, int PK>
 static ttt_status forward_t(const Call& c) {
     const Layout l = layout(c.d, PK == 3, false);
-    if constexpr (PK == 1) {
-        TcArgs a{};
-        if (use_tc(c) && tc_args(&a, c, false, c.ws + l.rec) && tc_outputs(&a, c.Z, c.d, nullptr, 0, nullptr)) {
-            a.W0 = c.W0;
-            a.w0_bs = c.w0_bs;
-            a.W1 = c.W1_out;
-            const ttt_status st = run_prep64<DK, false>(c, c.ws + l.rec);
-            return st != TTT_OK ? st : run_chain_tc<DK>(c, a);
-        }
-    }
     Splitter split{c, PK == 3};
     const Parts Q = split.add(c.Q, c.ws + l.qp, c.d.hk, DK), K = split.add(c.K, c.ws + l.kp, c.d.hk, DK);
     ttt_status st = split.run();
@@ -1084,7 +1094,7 @@ static ttt_status forward_t(const Call& c) {
     ChainOut out{};
     out.Z = c.Z;
     out.W1 = c.W1_out;
-    return few_tiles(c) ? run_chain_t<DK, P, PK, 1, 1>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 1>(c, Q, K, c.ws + l.rec, out);
+    return few_tiles(c) ? run_chain_t<DK, P, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
 }
 
 template <int DK, int P, int PK>
@@ -1109,39 +1119,20 @@ static ttt_status backward_t(const Call& c) {
                 O = split.add(c.Z, c.ws + l.op, c.d.h, c.d.dv);
     ttt_status st = split.run();
     if (st != TTT_OK) return st;
-    bool done = false;
-    if constexpr (PK == 1) {
-        TcArgs a{};
-        bool ok = use_tc(c) && tc_args(&a, c, true, rec);
-        TcArgs r = a;
-        ok = ok && map64(&r.V, O, c.d, c.d.h, c.d.dv) && tc_outputs(&a, c.dV, c.d, out.E, ps, out.S) && tc_outputs(&r, c.dV, c.d, bo.Y, ps, bo.D);
-        if (ok) {
-            a.W0 = c.W0;
-            a.w0_bs = c.w0_bs;
-            r.W0 = c.dW1;
-            r.w0_bs = (long long)c.d.h * c.d.dv * DK;
-            r.W1 = bo.dW0;
-            st = run_prep64<DK, true>(c, rec);
-            if (st == TTT_OK) st = run_both_tc<DK>(c, a, r);
-            done = true;
-        }
-    }
-    if (!done) {
-        st = run_prep<DK, P, PK, true>(c, Q, K, rec);
-        if (st == TTT_OK) st = run_both<DK, P, PK>(c, Q, K, O, rec, out, bo);
-    }
-    if (st == TTT_OK) st = run_grads<DK, P, PK>(c, Q, K, O, out, bo, reinterpret_cast<float*>(c.ws + l.part));
+    st = run_prep<DK, P, PK, true>(c, Q, K, rec);
+    if (st == TTT_OK) st = run_both<DK, P, PK>(c, Q, K, O, rec, out, bo);
+    if (st == TTT_OK) st = run_grads<DK, PK>(c, Q, K, O, out, bo, reinterpret_cast<float*>(c.ws + l.part));
     if (st != TTT_OK || !reduce) return st;
     return run_sum_images(bo.dW0, c.dW0, c.d.B, (long long)c.d.h * c.d.dv * DK, c.stream);
 }
 
 ttt_status launch_forward(const Call& c) {
-    if (c.fp32) return c.d.dk == 64 ? forward_t<64, 3, 3>(c) : forward_t<128, 3, 3>(c);
+    if (c.fp32) return c.d.dk == 64 ? forward_t<64, PF, 3>(c) : forward_t<128, PF, 3>(c);
     return c.d.dk == 64 ? forward_t<64, 2, 1>(c) : forward_t<128, 2, 1>(c);
 }
 ttt_status launch_backward(const Call& c) {
-    if (c.fp32) return c.d.dk == 64 ? backward_t<64, 3, 3>(c) : backward_t<128, 3, 3>(c);
-    return c.d.dk == 64 ? backward_t<64, 2, 1>(c) : backward_t<128, 2, 1>(c);
+    if (c.fp32) return c.d.dk == 64 ? backward_t<64, PF, 3>(c) : backward_t<128, PF, 3>(c);
+    return c.d.dk == 64 ? backward_t<64, PF, 1>(c) : backward_t<128, PF, 1>(c);
 }
 
 }  // namespace gd

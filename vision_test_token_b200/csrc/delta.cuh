@@ -35,11 +35,15 @@ struct Dims {
     float scale;
 };
 
+// bf16 parts of an operand that an fp32 result comes from: 24 bits, as many as fp32 has.
+constexpr int PF = 3;
 // Per (image, value head, chunk) record in the workspace, written by the prep kernel and copied as it
-// is into shared memory: gates (gamma, suffix, beta), then the bf16 part images of T', A and (backward) T_u.
+// is into shared memory: gates (gamma, suffix, beta), then the bf16 part images of T' (PF parts), A (P parts) and (backward)
+// T_u (PF parts).
 constexpr int kGateBytes = 3 * CT * 4;
 __host__ __device__ constexpr int mat_bytes(int P) { return P * CT * MP * 2; }
-__host__ __device__ constexpr int rec_bytes(int P, bool backward) { return kGateBytes + (backward ? 3 : 2) * mat_bytes(P); }
+constexpr int kRecA = kGateBytes + mat_bytes(PF);            // offset of A
+__host__ __device__ constexpr int rec_bytes(int P, bool backward) { return kRecA + mat_bytes(P) + (backward ? mat_bytes(PF) : 0); }
 
 struct Call {
     Dims d;

@@ -4,18 +4,21 @@
 //   reverse (two warps per 16 rows of D, sequential from the last chunk to the first):
 //     dU = diag(Gamma_C.) K D^T + A^T dZ,   Y = T_u^T dU  with T_u = (I + diag(beta) G)^{-1},
 //     dV = diag(beta) Y,   D <- gamma_C D + (diag(gamma) dZ')^T Q - (diag(gamma) dV)^T K;
-//   grads (one CTA per image, key head and group of tokens, all at once), from E, Y (per token), W at the
+//   grads (one CTA per image, value head and group of tokens, all at once), from E, Y (per token), W at the
 //     group's start and D at its end, with the group's own gamma and Gamma:
 //     H_ij = scale Gamma_ij beta_j dz_i.e_j (j <= i),   F_ij = -beta_i beta_j Gamma_ij y_i.e_j (j < i),
 //     dQ_i = scale gamma_i W^T dz_i + sum_j H_ij k_j,
 //     dK_i = beta_i Gamma_Ci D^T e_i - gamma_i beta_i W^T y_i + sum_j F_ij k_j + sum_j (H_ji q_j + F_ji k_j),
 //     dbeta_i = y_i.e_i,
-//     dg_l = gamma_C <D, W> + sum_{j<l} k_j.(first term of dK_j)
-//            + sum_{i>=l} (q_i.dQ_i + k_i.(second and third terms of dK_i) - k_i.(last term of dK_i)).
+//     dg_l = gamma_C <D, W> + sum_{j<l} k_j.(first term of dK_j) + sum_{i>=l} (q_i.(first term of dQ_i) + k_i.(second term of dK_i))
+//            + sum_{i>=l>j} (H_ij q_i.k_j + F_ij k_i.k_j).
+//   (Each term of dg_l is what one path through the gate of token l gives, so that all of them fade with the gate: sums over a token's own
+//   write and readout, which a strong gate does not touch, would leave only their rounding.)
 //   E and W come from the forward chain run again (they are not kept from the forward call).
 // The two sequential sweeps need nothing of each other and run side by side in one launch (24 ragged heads of up to
-// 1531 tokens, d = 128: 156 us one after the other, 116 us together).
-// All products take P bf16 parts per inexact operand, as the forward pass.
+// 1531 tokens, d = 128: 138 us).
+// Every inexact operand is three bf16 parts (for bf16 tokens two in H K, F K, H^T Q and F^T K, which end in dQ and dK alone, rounded to
+// eight bits).  Two parts throughout were off by 3e-6 (dW0) to 6e-6 (dbeta) in the 2-norm, a plain fp32 computation by 1 to 3e-7.
 
 struct BackOut {
     View dV;
@@ -31,6 +34,7 @@ struct ReverseLayout {
     static constexpr int kK = PK * CT * DK * 2;                // K, Q and T_u of the period's chunk,
     static constexpr int kO1 = CT * VB, kO = PK * kO1;         // dZ and A of the next one
     static constexpr int kM = mat_bytes(P);
+    static_assert(P == PF, "A and T_u have the same parts");
     static constexpr int stage = (2 * kK + kO + 2 * kM + 1023) / 1024 * 1024;
     static constexpr int kGates = kGateSlots * kGateBytes;
     static constexpr int kS = DK / 16 * P * 512;               // a tile's adjoint as operand parts
@@ -97,7 +101,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             if (now) {
                 load_tokens<DK, PK>(l, st, K, b, h / d.r, c * CT, len - c * CT);
                 load_tokens<DK, PK>(l, st + L::kK, Q, b, h / d.r, c * CT, len - c * CT);
-                l.flat(st + 2 * L::kK + L::kO, rec + ((long long)bh * d.nc + c) * recb + kGateBytes + 2 * L::kM, L::kM);
+                l.flat(st + 2 * L::kK + L::kO, rec + ((long long)bh * d.nc + c) * recb + kRecA + L::kM, L::kM);
             }
             if (next) {
                 const uint8_t* r = rec + ((long long)bh * d.nc + c - 1) * recb;
@@ -105,7 +109,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
                 for (int p = 0; p < PK; ++p)
                     l.template tile<L::VB, 2>(st + 2 * L::kK + p * L::kO1, O, p, b, h, (c - 1) * CT, v0, len - (c - 1) * CT);
                 l.flat(gate_slot(k + 1), r, kGateBytes);
-                l.flat(st + 2 * L::kK + L::kO + L::kM, r + kGateBytes + L::kM, L::kM);
+                l.flat(st + 2 * L::kK + L::kO + L::kM, r + kRecA, L::kM);
             }
         };
         for (int k = -1; k < L::kStages - 2; ++k) issue(k);
@@ -197,38 +201,37 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
         const bool hand = k == 0 || ((c + 1) * CT) % d.gt == 0;
 
         // dU = suffix (D K^T) + A^T dZ
-        float x[4][4] = {};
+        float x[4][4] = {}, low[4][4] = {};
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
             uint32_t a[P][4];
             as_operand<P>(a, s[2 * kk], s[2 * kk + 1]);
 #pragma unroll
-            for (int n2 = 0; n2 < 2; ++n2) dot_tokens<DK, P, PK>(x[2 * n2], x[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
+            for (int n2 = 0; n2 < 2; ++n2)
+                dot_tokens<DK, P, PK>(x[2 * n2], x[2 * n2 + 1], low[2 * n2], low[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
             if (hand) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) sts4u(sp + (((ks * KB + kk) * P + p) * 32 + lane) * 16, a[p]);
             }
         }
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[nb][q] += low[nb][q];
         if constexpr (KS > 1) {
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) sts4(xp + ((ks * 4 + nb) * 32 + lane) * 16, x[nb]);
         }
         // D <- gamma_C D + (scale gamma dZ)^T Q
-        const float gc = lds1(gt + (CT - 1) * 4);
+        uint32_t a[2][P][4];
 #pragma unroll
-        for (int nb = 0; nb < DW / 8; ++nb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) s[nb][q] *= gc;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            uint32_t a[P][4];
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const uint4 v = lds4u(fp + ((kk * P + p) * 32 + lane) * 16);
-                a[p][0] = v.x; a[p][1] = v.y; a[p][2] = v.z; a[p][3] = v.w;
+                a[kk][p][0] = v.x; a[kk][p][1] = v.y; a[kk][p][2] = v.z; a[kk][p][3] = v.w;
             }
-            add_outer<DK, DW, P, PK>(s, a, qt, kk, col0, lane);
-        }
+        fade_add_outer<DK, DW, P, PK>(s, lds1(gt + (CT - 1) * 4), a, qt, col0, lane);
         if constexpr (KS > 1) {
             tile_sync<KS>(rt);
 #pragma unroll
@@ -245,7 +248,6 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
         }
         // Y = T_u^T dU
         float y[4][4] = {};
-        uint32_t a[2][P][4];
         as_operand<P>(a[0], x[0], x[1]);
         as_operand<P>(a[1], x[2], x[3]);
 #pragma unroll
@@ -258,11 +260,9 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             const float u0 = -ga.x * be.x, u1 = -ga.y * be.y;
             y[nb][0] *= u0; y[nb][1] *= u1; y[nb][2] *= u0; y[nb][3] *= u1;
         }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            as_operand<P>(a[kk], y[2 * kk], y[2 * kk + 1]);
-            add_outer<DK, DW, P, PK>(s, a[kk], kt, kk, col0, lane);
-        }
+        as_operand<P>(a[0], y[0], y[1]);
+        as_operand<P>(a[1], y[2], y[3]);
+        fade_add_outer<DK, DW, P, PK>(s, 1.f, a, kt, col0, lane);
     }
     if (out.dW0) put_state<DK, DW>(s, out.dW0 + bh * state, row0, col0, lane);
 }
@@ -293,49 +293,94 @@ delta_both(const __grid_constant__ BothArgs a) {
 // --------------------------------------------------------------------------------------------------
 // Token gradients
 // --------------------------------------------------------------------------------------------------
-template <int DK, int P, int PK>
+template <int DK, int PK>
 struct GradsLayout {
+    static constexpr int PX = PK == 1 ? 2 : PF;                 // parts of what ends in gradients of the tokens' type alone
     static constexpr int GT = PK == 3 ? 32 : 64;                // tokens per group
     static constexpr int SV = 32;                               // value features per slice
     static constexpr int KP = DK + 8, SP = SV + 8, HP = GT + 8, FP = GT + 1;
     static constexpr int kK = PK * GT * KP * 2;                 // K, and Q
     static constexpr int kO = PK * GT * SP * 2;
-    static constexpr int kE = P * GT * SP * 2;                  // E, and Y
-    static constexpr int kS = P * SV * KP * 2;                  // W, and D
+    static constexpr int kE = PF * GT * SP * 2;                 // E, and Y
+    static constexpr int kS = PF * SV * KP * 2;                 // W, and D
     static constexpr int stage = kO + 2 * kE + 2 * kS;
-    static constexpr int kH = P * GT * HP * 2;                  // H, and F: in the stages' memory after the slices
-    static_assert(2 * kH <= 2 * stage, "H and F fit the stages");
-    static constexpr int kG = (GT * FP + 6 * GT + 4 * 8 * GT) * 4;   // Gamma, gate rows, reductions
+    static constexpr int kH = PX * GT * HP * 2;                // H, and F: in the stages' memory after the slices
+    static constexpr int WM = GT / 16, WN = 8 / WM;             // warps along the tokens, and along the columns
+    static constexpr int kRed = (2 * WN + WM) * GT + 8;         // partial row and column sums, then 8 warps' <D, W>
+    static constexpr int kG = (GT * FP + 5 * GT) * 4;           // Gamma, gate rows and dbeta
+    static_assert(2 * kH + kRed * 4 <= 2 * stage, "H, F and the sums fit the stages");
     static constexpr int smem = 2 * kK + 2 * stage + kG;
+    static_assert(smem <= 227 * 1024, "shared memory of a gradient CTA");
 };
 
-template <int DK, int P, int PK, bool GROUP>
+// (c0, c1) += a * (b[.][0], b[.][1]), (b[.][2], b[.][3]): the parts of 16 x 16 times 16 x 16, products of the parts below the P-th
+// dropped.  FRESH: summed in accumulators of their own, the small products first, and added in fp32.
+template <int P, bool FRESH, int NA, int NB>
+__device__ __forceinline__ void add_product(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4]) {
+    float u0[4] = {}, u1[4] = {};
+#pragma unroll
+    for (int order = P - 1; order >= 0; --order)
+#pragma unroll
+        for (int pb = 0; pb < NB; ++pb) {
+            const int pa = order - pb;
+            if (pa < 0 || pa >= NA) continue;
+            mma16816(FRESH ? u0 : c0, a[pa], b[pb][0], b[pb][1]);
+            mma16816(FRESH ? u1 : c1, a[pa], b[pb][2], b[pb][3]);
+        }
+    if (FRESH)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            c0[q] += u0[q];
+            c1[q] += u1[q];
+        }
+}
+
+struct GradsArgs {
+    Dims d;
+    Parts Q, K, O;
+    View G, Beta;
+    const __nv_bfloat16 *E, *Y;       // [PF][B][h][N][dv], parts eps apart
+    long long eps;
+    const __nv_bfloat16 *S, *D;       // states at the groups' starts, adjoints at their ends [B][h][ng][PF][dv][dk]
+    View dQ, dK, dG, dBeta;
+    float* part;                      // nullable: fp32 dQ, then dK, per value head [2][B][h][N][dk] instead
+};
+
+// Bound: latency, one CTA of eight warps per SM (the matrix instructions of a group are about 160 us of the following).  32 heads of
+// 4096 tokens, d = 128: 450 us.
+template <int DK, int PK>
 __global__ void __launch_bounds__(256)
-delta_grads(Dims d, Parts Q, Parts K, Parts O, View G, View Beta, const __nv_bfloat16* E, const __nv_bfloat16* Y, long long eps,
-            const __nv_bfloat16* S, const __nv_bfloat16* D, View dQ, View dK, View dG, View dBeta) {
-    using L = GradsLayout<DK, P, PK>;
-    constexpr int GT = L::GT, SV = L::SV, KP = L::KP, SP = L::SP, HP = L::HP, FP = L::FP, NT = 256;
-    constexpr int WM = GT / 16, WN = 8 / WM, NBA = GT / WN / 8, DKW = DK / WN, NBK = DKW / 8;
+delta_grads(const __grid_constant__ GradsArgs p) {
+    using L = GradsLayout<DK, PK>;
+    constexpr int PX = L::PX, GT = L::GT, SV = L::SV, KP = L::KP, SP = L::SP, HP = L::HP, FP = L::FP, NT = 256;
+    constexpr int WM = L::WM, WN = L::WN, NBA = GT / WN / 8, DKW = DK / WN, NBK = DKW / 8;
+    constexpr bool FX = PK == 3;                                // dK is fp32 too
     extern __shared__ __align__(16) uint8_t smem[];
+    const Dims& d = p.d;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int mi = lane >> 3, lr = lane & 7;
     const int wm = warp % WM, wn = warp / WM;
     pdl_launch_dependents();
     pdl_wait_primary();
     const int grp = blockIdx.x % d.ng;
-    const int bk = blockIdx.x / d.ng, b = bk / d.hk, kh = bk % d.hk;
+    const long long bh = blockIdx.x / d.ng;
+    const int h = (int)(bh % d.h), b = (int)(bh / d.h), kh = h / d.r;
     const int left = min(GT, seq_len(d, b) - grp * GT);
     if (left <= 0) return;
     const long long tok = (long long)grp * GT;
     const uint32_t sb = s32(smem), kt = sb, qt = sb + L::kK, st0 = sb + 2 * L::kK;
-    uint8_t* tail = smem + 2 * L::kK + 2 * L::stage;
-    float* gam2 = reinterpret_cast<float*>(tail);               // Gamma [GT][FP]
-    float* gl = gam2 + GT * FP;                                 // g, gamma, suffix, beta, dbeta, kappa
+    float* gam2 = reinterpret_cast<float*>(smem + 2 * L::kK + 2 * L::stage);   // Gamma [GT][FP]
+    float* gl = gam2 + GT * FP;                                 // g, gamma, suffix, beta, dbeta
     float* ga = gl + GT;
     float* su = ga + GT;
     float* be = su + GT;
     float* dbe = be + GT;
-    float* red = dbe + 2 * GT;                                  // [3][WN][GT] partial dots, then 8 warps' <D, W>
+    uint8_t* hs = smem + 2 * L::kK;                             // H, F, and the sums, once the slices are done
+    uint8_t* fs = hs + L::kH;
+    float* rows_sum = reinterpret_cast<float*>(fs + L::kH);     // [WN][GT] row terms, [WN][GT] k.(first term of dK)
+    float* kap_sum = rows_sum + WN * GT;
+    float* cols_sum = kap_sum + WN * GT;                        // [WM][GT] column sums
+    float* dots = cols_sum + WM * GT;
 
     auto rows = [&](uint32_t dst, int pitch, const __nv_bfloat16* src, long long ts, int width) {
         const int cpr = width / 8;
@@ -346,346 +391,330 @@ delta_grads(Dims d, Parts Q, Parts K, Parts O, View G, View Beta, const __nv_bfl
         }
     };
 #pragma unroll
-    for (int p = 0; p < PK; ++p) {
-        rows(kt + p * GT * KP * 2, KP, K.p + p * K.ps + b * K.bs + kh * K.hs + tok * K.ts, K.ts, DK);
-        rows(qt + p * GT * KP * 2, KP, Q.p + p * Q.ps + b * Q.bs + kh * Q.hs + tok * Q.ts, Q.ts, DK);
-    }
-    float tq[GROUP ? NBK : 1][4], tk[GROUP ? NBK : 1][4];
-    if constexpr (GROUP) {
-#pragma unroll
-        for (int nb = 0; nb < NBK; ++nb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tq[nb][q] = tk[nb][q] = 0.f;
+    for (int q = 0; q < PK; ++q) {
+        rows(kt + q * GT * KP * 2, KP, p.K.p + q * p.K.ps + b * p.K.bs + kh * p.K.hs + tok * p.K.ts, p.K.ts, DK);
+        rows(qt + q * GT * KP * 2, KP, p.Q.p + q * p.Q.ps + b * p.Q.bs + kh * p.Q.hs + tok * p.Q.ts, p.Q.ts, DK);
     }
     const int ns = d.dv / SV;
-    const long long state = (long long)d.dv * DK;
+    const long long state = (long long)d.dv * DK, so0 = (bh * d.ng + grp) * PF * state;
     const int i0 = wm * 16 + g;                                 // this lane's rows: i0, i0 + 8
 
-    for (int rr = 0; rr < (GROUP ? d.r : 1); ++rr) {
-        const int h = kh * d.r + rr;
-        const long long bh = (long long)b * d.h + h;
-        auto issue = [&](int sl) {
-            if (sl < ns) {
-                const uint32_t st = st0 + (sl & 1) * L::stage;
+    auto issue = [&](int sl) {
+        if (sl < ns) {
+            const uint32_t st = st0 + (sl & 1) * L::stage, et = st + L::kO, yt = et + L::kE, wt = yt + L::kE, dt = wt + L::kS;
 #pragma unroll
-                for (int p = 0; p < PK; ++p)
-                    rows(st + p * GT * SP * 2, SP, O.p + p * O.ps + b * O.bs + h * O.hs + tok * O.ts + sl * SV, O.ts, SV);
+            for (int q = 0; q < PK; ++q)
+                rows(st + q * GT * SP * 2, SP, p.O.p + q * p.O.ps + b * p.O.bs + h * p.O.hs + tok * p.O.ts + sl * SV, p.O.ts, SV);
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const long long eo = p * eps + (bh * d.N + tok) * d.dv + sl * SV;
-                    rows(st + L::kO + p * GT * SP * 2, SP, E + eo, d.dv, SV);
-                    rows(st + L::kO + L::kE + p * GT * SP * 2, SP, Y + eo, d.dv, SV);
-                    const long long so = ((bh * d.ng + grp) * P + p) * state + (long long)sl * SV * DK;
-                    for (int x = tid; x < SV * DK / 8; x += NT) {
-                        const int row = x / (DK / 8), col = x % (DK / 8);
-                        const uint32_t to = (p * SV * KP + row * KP + col * 8) * 2;
-                        cp16(st + L::kO + 2 * L::kE + to, S + so + row * DK + col * 8, true);
-                        cp16(st + L::kO + 2 * L::kE + L::kS + to, D + so + row * DK + col * 8, true);
-                    }
+            for (int q = 0; q < PF; ++q) {
+                const long long eo = q * p.eps + (bh * d.N + tok) * d.dv + sl * SV;
+                rows(et + q * GT * SP * 2, SP, p.E + eo, d.dv, SV);
+                rows(yt + q * GT * SP * 2, SP, p.Y + eo, d.dv, SV);
+                const long long so = so0 + q * state + (long long)sl * SV * DK;
+                for (int x = tid; x < SV * DK / 8; x += NT) {
+                    const int row = x / (DK / 8), col = x % (DK / 8);
+                    const uint32_t to = (q * SV * KP + row * KP + col * 8) * 2;
+                    cp16(wt + to, p.S + so + row * DK + col * 8, true);
+                    cp16(dt + to, p.D + so + row * DK + col * 8, true);
                 }
             }
-            cp_commit();
-        };
-        issue(0);
-        issue(1);
-        if (tid < GT) {
-            const bool live = tid < left;
-            gl[tid] = live ? reinterpret_cast<const float*>(G.p)[b * G.bs + h * G.hs + (tok + tid) * G.ts] : 0.f;
-            be[tid] = live ? reinterpret_cast<const float*>(Beta.p)[b * Beta.bs + h * Beta.hs + (tok + tid) * Beta.ts] : 0.f;
+        }
+        cp_commit();
+    };
+    issue(0);
+    issue(1);
+    if (tid < GT) {
+        const bool live = tid < left;
+        gl[tid] = live ? reinterpret_cast<const float*>(p.G.p)[b * p.G.bs + h * p.G.hs + (tok + tid) * p.G.ts] : 0.f;
+        be[tid] = live ? reinterpret_cast<const float*>(p.Beta.p)[b * p.Beta.bs + h * p.Beta.hs + (tok + tid) * p.Beta.ts] : 0.f;
+    }
+    __syncthreads();
+    if (tid < GT) {
+        float a = 0.f, z = 0.f;
+        for (int i = 0; i <= tid; ++i) a += gl[i];
+        for (int i = GT - 1; i > tid; --i) z += gl[i];
+        ga[tid] = expf(a);
+        su[tid] = expf(z);
+    }
+    {
+        constexpr int PARTS = NT / GT, RP = GT / PARTS;         // row ranges per column
+        const int j = tid % GT, r0 = tid / GT * RP;
+        float a = 0.f;
+        for (int i = j + 1; i < r0; ++i) a += gl[i];
+        for (int i = r0; i < r0 + RP; ++i) {
+            if (i > j) a += gl[i];
+            gam2[i * FP + j] = i >= j ? expf(a) : 0.f;
+        }
+    }
+    float aq[NBA][4] = {}, al[NBA][4] = {};                     // dZ E^T, Y E^T
+    float fq[NBK][4] = {}, f4[NBK][4] = {}, f5[NBK][4] = {};    // dZ W, E D, Y W
+    float dot = 0.f;
+    // 16 x 16 blocks (8 columns where a warp has no more) of the token by token matrices: this warp's are n = 0, 2, ..
+    constexpr int NB2 = NBA > 1 ? 2 : 1;
+    auto columns = [&](uint32_t (&x)[4], uint32_t tile, int pitch, int nb, int kk) {
+        const int j0 = wn * (GT / WN) + nb * 8;
+        if constexpr (NB2 == 2) {
+            ldsm4(x, tile + ((j0 + (mi >> 1) * 8 + lr) * pitch + kk * 16 + (mi & 1) * 8) * 2);
+        } else {
+            asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+                         : "=r"(x[0]), "=r"(x[1])
+                         : "r"(tile + ((j0 + lr) * pitch + kk * 16 + (mi & 1) * 8) * 2)
+                         : "memory");
+            x[2] = x[3] = 0;
+        }
+    };
+    float none[4] = {};
+    for (int sl = 0; sl < ns; ++sl) {
+        cp_wait<1>();
+        __syncthreads();
+        const uint32_t ot = st0 + (sl & 1) * L::stage, et = ot + L::kO, yt = et + L::kE, wt = yt + L::kE, dt = wt + L::kS;
+        const uint32_t arow = ((wm * 16 + (mi & 1) * 8 + lr) * SP + (mi >> 1) * 8) * 2;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            uint32_t ao[PK][4], ae[PF][4], ay[PF][4];
+#pragma unroll
+            for (int q = 0; q < PK; ++q) ldsm4(ao[q], ot + q * GT * SP * 2 + arow + kk * 32);
+#pragma unroll
+            for (int q = 0; q < PF; ++q) {
+                ldsm4(ae[q], et + q * GT * SP * 2 + arow + kk * 32);
+                ldsm4(ay[q], yt + q * GT * SP * 2 + arow + kk * 32);
+            }
+#pragma unroll
+            for (int n2 = 0; n2 < NBK / 2; ++n2) {
+                const uint32_t bo = ((kk * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2;
+                uint32_t w[PF][4];
+#pragma unroll
+                for (int q = 0; q < PF; ++q) ldsm4t(w[q], wt + q * SV * KP * 2 + bo);
+                add_product<PF, true>(fq[2 * n2], fq[2 * n2 + 1], ao, w);
+                add_product<PF, true>(f5[2 * n2], f5[2 * n2 + 1], ay, w);
+#pragma unroll
+                for (int q = 0; q < PF; ++q) ldsm4t(w[q], dt + q * SV * KP * 2 + bo);
+                add_product<PF, true>(f4[2 * n2], f4[2 * n2 + 1], ae, w);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NBA; nb += NB2) {
+                if (wn * (GT / WN) + nb * 8 > wm * 16 + 15) continue;
+                uint32_t x[PF][4];
+#pragma unroll
+                for (int q = 0; q < PF; ++q) columns(x[q], et + q * GT * SP * 2, SP, nb, kk);
+                add_product<PF, true>(aq[nb], NB2 > 1 ? aq[nb + NB2 - 1] : none, ao, x);
+                add_product<PF, true>(al[nb], NB2 > 1 ? al[nb + NB2 - 1] : none, ay, x);
+            }
+        }
+        for (int x = tid; x < SV * DK / 2; x += NT) {           // <D, W> of the slice
+            const uint32_t o = (x / (DK / 2) * KP + x % (DK / 2) * 2) * 2;
+            float w0 = 0.f, w1 = 0.f, d0 = 0.f, d1 = 0.f;
+#pragma unroll
+            for (int q = PF - 1; q >= 0; --q) {
+                const uint32_t a = *reinterpret_cast<const uint32_t*>(smem + (wt - sb) + q * SV * KP * 2 + o);
+                const uint32_t z = *reinterpret_cast<const uint32_t*>(smem + (dt - sb) + q * SV * KP * 2 + o);
+                w0 += lo_f(a); w1 += hi_f(a); d0 += lo_f(z); d1 += hi_f(z);
+            }
+            dot = fmaf(w0, d0, fmaf(w1, d1, dot));
         }
         __syncthreads();
-        if (tid < GT) {
-            float a = 0.f, z = 0.f;
-            for (int i = 0; i <= tid; ++i) a += gl[i];
-            for (int i = GT - 1; i > tid; --i) z += gl[i];
-            ga[tid] = expf(a);
-            su[tid] = expf(z);
-        }
-        {
-            constexpr int PARTS = NT / GT, RP = GT / PARTS;     // row ranges per column
-            const int j = tid % GT, r0 = tid / GT * RP;
-            float a = 0.f;
-            for (int i = j + 1; i < r0; ++i) a += gl[i];
-            for (int i = r0; i < r0 + RP; ++i) {
-                if (i > j) a += gl[i];
-                gam2[i * FP + j] = i >= j ? expf(a) : 0.f;
+        issue(sl + 2);
+    }
+    cp_wait<0>();
+    // H, F as bf16 parts in shared memory; dbeta from the diagonal of Y E^T; the sums of H_ij q_i.k_j + F_ij k_i.k_j along rows and columns
+    const uint32_t ht = s32(hs), ft = s32(fs);
+    float rho[2] = {}, kap[2] = {};
+#pragma unroll
+    for (int nb = 0; nb < NBA; nb += NB2) {
+        float qk[2][4] = {}, kk2[2][4] = {};
+        if (wn * (GT / WN) + nb * 8 <= wm * 16 + 15) {
+            const uint32_t arow = ((wm * 16 + (mi & 1) * 8 + lr) * KP + (mi >> 1) * 8) * 2;
+#pragma unroll(PK == 1 ? 4 : 1)
+            for (int kk = 0; kk < DK / 16; ++kk) {
+                uint32_t x[PK][4], a[PK][4];
+#pragma unroll
+                for (int q = 0; q < PK; ++q) {
+                    columns(x[q], kt + q * GT * KP * 2, KP, nb, kk);
+                    ldsm4(a[q], qt + q * GT * KP * 2 + arow + kk * 32);
+                }
+                add_product<PK, PK == 3>(qk[0], qk[1], a, x);
+#pragma unroll
+                for (int q = 0; q < PK; ++q) ldsm4(a[q], kt + q * GT * KP * 2 + arow + kk * 32);
+                add_product<PK, PK == 3>(kk2[0], kk2[1], a, x);
             }
         }
-        float aq[NBA][4] = {}, al[NBA][4] = {};                 // dZ E^T, Y E^T
-        float fq[NBK][4] = {}, f4[NBK][4] = {}, f5[NBK][4] = {};  // dZ W, E D, Y W
-        float dot = 0.f;
-        for (int sl = 0; sl < ns; ++sl) {
-            cp_wait<1>();
-            __syncthreads();
-            const uint32_t ot = st0 + (sl & 1) * L::stage, et = ot + L::kO, yt = et + L::kE, wt = yt + L::kE, dt = wt + L::kS;
-            const uint32_t arow = ((wm * 16 + (mi & 1) * 8 + lr) * SP + (mi >> 1) * 8) * 2;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                uint32_t ao[PK][4], ae[P][4], ay[P][4];
-#pragma unroll
-                for (int p = 0; p < PK; ++p) ldsm4(ao[p], ot + p * GT * SP * 2 + arow + kk * 32);
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    ldsm4(ae[p], et + p * GT * SP * 2 + arow + kk * 32);
-                    ldsm4(ay[p], yt + p * GT * SP * 2 + arow + kk * 32);
-                }
-#pragma unroll
-                for (int n2 = 0; n2 < NBK / 2; ++n2) {
-                    const uint32_t bo = ((kk * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2;
-#pragma unroll
-                    for (int pb = 0; pb < P; ++pb) {
-                        uint32_t w[4];
-                        ldsm4t(w, wt + pb * SV * KP * 2 + bo);
-#pragma unroll
-                        for (int pa = 0; pa < PK; ++pa)
-                            if (pa + pb < P) {
-                                mma16816(fq[2 * n2], ao[pa], w[0], w[1]);
-                                mma16816(fq[2 * n2 + 1], ao[pa], w[2], w[3]);
-                            }
-#pragma unroll
-                        for (int pa = 0; pa + pb < P; ++pa) {
-                            mma16816(f5[2 * n2], ay[pa], w[0], w[1]);
-                            mma16816(f5[2 * n2 + 1], ay[pa], w[2], w[3]);
-                        }
-                        ldsm4t(w, dt + pb * SV * KP * 2 + bo);
-#pragma unroll
-                        for (int pa = 0; pa + pb < P; ++pa) {
-                            mma16816(f4[2 * n2], ae[pa], w[0], w[1]);
-                            mma16816(f4[2 * n2 + 1], ae[pa], w[2], w[3]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int nb = 0; nb < NBA; ++nb) {
-                    const int j0 = wn * (GT / WN) + nb * 8;
-                    if (j0 <= wm * 16 + 15) {
-#pragma unroll
-                        for (int pb = 0; pb < P; ++pb) {
-                            uint32_t b0, b1;
-                            asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-                                         : "=r"(b0), "=r"(b1)
-                                         : "r"(et + ((pb * GT + j0 + lr) * SP + kk * 16 + (mi & 1) * 8) * 2)
-                                         : "memory");
-#pragma unroll
-                            for (int pa = 0; pa < PK; ++pa)
-                                if (pa + pb < P) mma16816(aq[nb], ao[pa], b0, b1);
-#pragma unroll
-                            for (int pa = 0; pa + pb < P; ++pa) mma16816(al[nb], ay[pa], b0, b1);
-                        }
-                    }
-                }
-            }
-            for (int x = tid; x < SV * DK / 2; x += NT) {       // <D, W> of the slice
-                const uint32_t o = (x / (DK / 2) * KP + x % (DK / 2) * 2) * 2;
-                float w0 = 0.f, w1 = 0.f, d0 = 0.f, d1 = 0.f;
-#pragma unroll
-                for (int p = P - 1; p >= 0; --p) {
-                    const uint32_t a = *reinterpret_cast<const uint32_t*>(smem + (wt - sb) + p * SV * KP * 2 + o);
-                    const uint32_t z = *reinterpret_cast<const uint32_t*>(smem + (dt - sb) + p * SV * KP * 2 + o);
-                    w0 += lo_f(a); w1 += hi_f(a); d0 += lo_f(z); d1 += hi_f(z);
-                }
-                dot = fmaf(w0, d0, fmaf(w1, d1, dot));
-            }
-            __syncthreads();
-            issue(sl + 2);
-        }
-        cp_wait<0>();
-        // H, F as bf16 parts in shared memory; dbeta from the diagonal of Y E^T
-        uint8_t* hs = smem + 2 * L::kK;
-        uint8_t* fs = hs + L::kH;
-        const uint32_t ht = s32(hs), ft = s32(fs);
-#pragma unroll
-        for (int nb = 0; nb < NBA; ++nb)
+        for (int n = 0; n < NB2; ++n) {
+            const int j = wn * (GT / WN) + (nb + n) * 8 + 2 * t;
+            float col[2] = {};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int i = i0 + 8 * half, j = wn * (GT / WN) + nb * 8 + 2 * t;
+                const int i = i0 + 8 * half;
                 float hv[2], fv[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float gm = gam2[i * FP + j + q], bj = be[j + q];
-                    if (i == j + q) dbe[i] = al[nb][2 * half + q];
-                    hv[q] = i >= j + q ? d.scale * gm * bj * aq[nb][2 * half + q] : 0.f;
-                    fv[q] = i > j + q ? -be[i] * bj * gm * al[nb][2 * half + q] : 0.f;
+                    const float gm = gam2[i * FP + j + q], bj = be[j + q], y = al[nb + n][2 * half + q];
+                    if (i == j + q) dbe[i] = y;
+                    hv[q] = i >= j + q ? d.scale * gm * bj * aq[nb + n][2 * half + q] : 0.f;
+                    fv[q] = i > j + q ? -be[i] * bj * gm * y : 0.f;
+                    const float pair = i > j + q ? hv[q] * qk[n][2 * half + q] + fv[q] * kk2[n][2 * half + q] : 0.f;
+                    rho[half] += pair;
+                    col[q] += pair;
                 }
-                uint32_t o[P];
-                split2<P>(hv[0], hv[1], o);
+                uint32_t o[PX], f[PX];
+                split2<PX>(hv[0], hv[1], o);
 #pragma unroll
-                for (int p = 0; p < P; ++p) *reinterpret_cast<uint32_t*>(hs + ((p * GT + i) * HP + j) * 2) = o[p];
-                split2<P>(fv[0], fv[1], o);
+                for (int q = 0; q < PX; ++q) *reinterpret_cast<uint32_t*>(hs + ((q * GT + i) * HP + j) * 2) = o[q];
+                split2<PX>(fv[0], fv[1], f);
 #pragma unroll
-                for (int p = 0; p < P; ++p) *reinterpret_cast<uint32_t*>(fs + ((p * GT + i) * HP + j) * 2) = o[p];
-            }
-        dot += __shfl_xor_sync(~0u, dot, 16);
-        dot += __shfl_xor_sync(~0u, dot, 8);
-        dot += __shfl_xor_sync(~0u, dot, 4);
-        dot += __shfl_xor_sync(~0u, dot, 2);
-        dot += __shfl_xor_sync(~0u, dot, 1);
-        if (lane == 0) red[3 * WN * GT + warp] = dot;
-        __syncthreads();
-        // dQ: scale gamma (dZ W) + H K;  second and third terms of dK: -gamma beta (Y W) + F K
-        {
-            const float a0 = d.scale * ga[i0], a1 = d.scale * ga[i0 + 8];
-            const float c0 = -ga[i0] * be[i0], c1 = -ga[i0 + 8] * be[i0 + 8];
-            const float e0 = be[i0] * su[i0], e1 = be[i0 + 8] * su[i0 + 8];
-#pragma unroll
-            for (int nb = 0; nb < NBK; ++nb) {
-                fq[nb][0] *= a0; fq[nb][1] *= a0; fq[nb][2] *= a1; fq[nb][3] *= a1;
-                f5[nb][0] *= c0; f5[nb][1] *= c0; f5[nb][2] *= c1; f5[nb][3] *= c1;
-                f4[nb][0] *= e0; f4[nb][1] *= e0; f4[nb][2] *= e1; f4[nb][3] *= e1;
-            }
-        }
-        for (int jj = 0; jj <= wm; ++jj) {
-            uint32_t ah[P][4], af[P][4];
-            const uint32_t ao = ((wm * 16 + (mi & 1) * 8 + lr) * HP + jj * 16 + (mi >> 1) * 8) * 2;
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                ldsm4(ah[p], ht + p * GT * HP * 2 + ao);
-                ldsm4(af[p], ft + p * GT * HP * 2 + ao);
+                for (int q = 0; q < PX; ++q) *reinterpret_cast<uint32_t*>(fs + ((q * GT + i) * HP + j) * 2) = f[q];
             }
 #pragma unroll
-            for (int n2 = 0; n2 < NBK / 2; ++n2)
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                for (int pb = 0; pb < PK; ++pb) {
-                    uint32_t w[4];
-                    ldsm4t(w, kt + ((pb * GT + jj * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2);
-#pragma unroll
-                    for (int pa = 0; pa + pb < P; ++pa) {
-                        mma16816(fq[2 * n2], ah[pa], w[0], w[1]);
-                        mma16816(fq[2 * n2 + 1], ah[pa], w[2], w[3]);
-                        mma16816(f5[2 * n2], af[pa], w[0], w[1]);
-                        mma16816(f5[2 * n2 + 1], af[pa], w[2], w[3]);
-                    }
-                }
-        }
-        // row dots with q and k
-        float rho[2] = {}, kap[2] = {}, chi[2] = {};
-        auto token2 = [&](uint32_t tile, int row, int col) {    // (x[row][col], x[row][col + 1]) of a token tile
-            float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int p = PK - 1; p >= 0; --p) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + (tile - sb) + ((p * GT + row) * KP + col) * 2);
-                v.x += lo_f(w);
-                v.y += hi_f(w);
+                for (int o = 4; o < 32; o *= 2) col[q] += __shfl_xor_sync(~0u, col[q], o);
+                if (g == 0) cols_sum[wm * GT + j + q] = col[q];
             }
-            return v;
-        };
-#pragma unroll
-        for (int nb = 0; nb < NBK; ++nb)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int col = wn * DKW + nb * 8 + 2 * t;
-                const float2 q = token2(qt, i0 + 8 * half, col), k = token2(kt, i0 + 8 * half, col);
-                rho[half] += q.x * fq[nb][2 * half] + q.y * fq[nb][2 * half + 1] + k.x * f5[nb][2 * half] + k.y * f5[nb][2 * half + 1];
-                kap[half] += k.x * f4[nb][2 * half] + k.y * f4[nb][2 * half + 1];
-                f5[nb][2 * half] += f4[nb][2 * half];
-                f5[nb][2 * half + 1] += f4[nb][2 * half + 1];
-                f4[nb][2 * half] = f4[nb][2 * half + 1] = 0.f;
-            }
-        // last term of dK: H^T Q + F^T K
-        for (int ii = wm; ii < WM; ++ii) {
-            uint32_t ah[P][4], af[P][4];
-            const uint32_t ao = ((ii * 16 + (mi >> 1) * 8 + lr) * HP + wm * 16 + (mi & 1) * 8) * 2;
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                ldsm4t(ah[p], ht + p * GT * HP * 2 + ao);
-                ldsm4t(af[p], ft + p * GT * HP * 2 + ao);
-            }
-#pragma unroll
-            for (int n2 = 0; n2 < NBK / 2; ++n2)
-#pragma unroll
-                for (int pb = 0; pb < PK; ++pb) {
-                    uint32_t w[4];
-                    const uint32_t bo = ((pb * GT + ii * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2;
-                    ldsm4t(w, qt + bo);
-#pragma unroll
-                    for (int pa = 0; pa + pb < P; ++pa) {
-                        mma16816(f4[2 * n2], ah[pa], w[0], w[1]);
-                        mma16816(f4[2 * n2 + 1], ah[pa], w[2], w[3]);
-                    }
-                    ldsm4t(w, kt + bo);
-#pragma unroll
-                    for (int pa = 0; pa + pb < P; ++pa) {
-                        mma16816(f4[2 * n2], af[pa], w[0], w[1]);
-                        mma16816(f4[2 * n2 + 1], af[pa], w[2], w[3]);
-                    }
-                }
-        }
-#pragma unroll
-        for (int nb = 0; nb < NBK; ++nb)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float2 k = token2(kt, i0 + 8 * half, wn * DKW + nb * 8 + 2 * t);
-                chi[half] += k.x * f4[nb][2 * half] + k.y * f4[nb][2 * half + 1];
-                f5[nb][2 * half] += f4[nb][2 * half];
-                f5[nb][2 * half + 1] += f4[nb][2 * half + 1];
-            }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int o = 1; o < 4; o *= 2) {
-                rho[half] += __shfl_xor_sync(~0u, rho[half], o);
-                kap[half] += __shfl_xor_sync(~0u, kap[half], o);
-                chi[half] += __shfl_xor_sync(~0u, chi[half], o);
-            }
-            if (t == 0) {
-                red[wn * GT + i0 + 8 * half] = rho[half];
-                red[(WN + wn) * GT + i0 + 8 * half] = kap[half];
-                red[(2 * WN + wn) * GT + i0 + 8 * half] = chi[half];
-            }
-        }
-        __syncthreads();
-        if (tid < GT) {                                         // sums over the column warps, in order
-            float a = 0.f, k = 0.f, x = 0.f;
-            for (int w = 0; w < WN; ++w) {
-                a += red[w * GT + tid];
-                k += red[(WN + w) * GT + tid];
-                x += red[(2 * WN + w) * GT + tid];
-            }
-            gl[tid] = a - x;                                    // g is no longer needed
-            dbe[GT + tid] = k;
-        }
-        __syncthreads();
-        if (tid < left) {
-            float a = 0.f;
-            for (int w = 0; w < 8; ++w) a += red[3 * WN * GT + w];
-            a *= ga[GT - 1];
-            for (int j = 0; j < tid; ++j) a += dbe[GT + j];
-            for (int i = tid; i < GT; ++i) a += gl[i];
-            reinterpret_cast<float*>(dG.p)[b * dG.bs + h * dG.hs + (tok + tid) * dG.ts] = a;
-            reinterpret_cast<float*>(dBeta.p)[b * dBeta.bs + h * dBeta.hs + (tok + tid) * dBeta.ts] = dbe[tid];
-        }
-        if constexpr (GROUP) {
-#pragma unroll
-            for (int nb = 0; nb < NBK; ++nb)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tq[nb][q] += fq[nb][q];
-                    tk[nb][q] += f5[nb][q];
-                }
-            __syncthreads();                                    // the stages and gate rows are written again
-        }
-        if (!GROUP || rr == d.r - 1) {
-#pragma unroll
-            for (int nb = 0; nb < NBK; ++nb)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int i = i0 + 8 * half, col = wn * DKW + nb * 8 + 2 * t;
-                    if (i >= left) continue;
-                    const long long qo = b * dQ.bs + kh * dQ.hs + (tok + i) * dQ.ts + col, ko = b * dK.bs + kh * dK.hs + (tok + i) * dK.ts + col;
-                    const float q0 = GROUP ? tq[GROUP ? nb : 0][2 * half] : fq[nb][2 * half];
-                    const float q1 = GROUP ? tq[GROUP ? nb : 0][2 * half + 1] : fq[nb][2 * half + 1];
-                    const float k0 = GROUP ? tk[GROUP ? nb : 0][2 * half] : f5[nb][2 * half];
-                    const float k1 = GROUP ? tk[GROUP ? nb : 0][2 * half + 1] : f5[nb][2 * half + 1];
-                    if constexpr (PK == 1) {
-                        *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(dQ.p) + qo) = pack2(q0, q1);
-                        *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(dK.p) + ko) = pack2(k0, k1);
-                    } else {
-                        *reinterpret_cast<float2*>(reinterpret_cast<float*>(dQ.p) + qo) = make_float2(q0, q1);
-                        *reinterpret_cast<float2*>(reinterpret_cast<float*>(dK.p) + ko) = make_float2(k0, k1);
-                    }
-                }
         }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) dot += __shfl_xor_sync(~0u, dot, o);
+    if (lane == 0) dots[warp] = dot;
+    // First terms: scale gamma (dZ W) of dQ, beta suffix (E D) and -gamma beta (Y W) of dK, and their row dots with q and k
+    auto token2 = [&](uint32_t tile, int row, int col) {        // (x[row][col], x[row][col + 1]) of a token tile
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = PK - 1; q >= 0; --q) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + (tile - sb) + ((q * GT + row) * KP + col) * 2);
+            v.x += lo_f(w);
+            v.y += hi_f(w);
+        }
+        return v;
+    };
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int i = i0 + 8 * half;
+        const float fa = d.scale * ga[i], fc = -ga[i] * be[i], fe = be[i] * su[i];
+#pragma unroll
+        for (int nb = 0; nb < NBK; ++nb) {
+            const int col = wn * DKW + nb * 8 + 2 * t;
+            const float2 q = token2(qt, i, col), k = token2(kt, i, col);
+            float *x = &fq[nb][2 * half], *y = &f5[nb][2 * half], *z = &f4[nb][2 * half];
+            x[0] *= fa; x[1] *= fa; y[0] *= fc; y[1] *= fc; z[0] *= fe; z[1] *= fe;
+            rho[half] += (q.x * x[0] + q.y * x[1]) + (k.x * y[0] + k.y * y[1]);
+            kap[half] += k.x * z[0] + k.y * z[1];
+            y[0] += z[0]; y[1] += z[1];
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+            rho[half] += __shfl_xor_sync(~0u, rho[half], o);
+            kap[half] += __shfl_xor_sync(~0u, kap[half], o);
+        }
+        if (t == 0) {
+            rows_sum[wn * GT + i] = rho[half];
+            kap_sum[wn * GT + i] = kap[half];
+        }
+    }
+    __syncthreads();
+    if (tid < GT) {                                             // sums over the warps, in order
+        float a = 0.f, k = 0.f;
+        for (int w = 0; w < WN; ++w) {
+            a += rows_sum[w * GT + tid];
+            k += kap_sum[w * GT + tid];
+        }
+        for (int w = 0; w < WM; ++w) a -= cols_sum[w * GT + tid];
+        gl[tid] = a;                                            // g and the suffixes are no longer needed
+        su[tid] = k;
+    }
+    for (int jj = 0; jj <= wm; ++jj) {                          // H K, F K
+        uint32_t ah[PX][4], af[PX][4];
+        const uint32_t ao = ((wm * 16 + (mi & 1) * 8 + lr) * HP + jj * 16 + (mi >> 1) * 8) * 2;
+#pragma unroll
+        for (int q = 0; q < PX; ++q) {
+            ldsm4(ah[q], ht + q * GT * HP * 2 + ao);
+            ldsm4(af[q], ft + q * GT * HP * 2 + ao);
+        }
+#pragma unroll
+        for (int n2 = 0; n2 < NBK / 2; ++n2) {
+            uint32_t w[PK][4];
+#pragma unroll
+            for (int q = 0; q < PK; ++q)
+                ldsm4t(w[q], kt + ((q * GT + jj * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2);
+            add_product<PX, FX>(fq[2 * n2], fq[2 * n2 + 1], ah, w);
+            add_product<PX, FX>(f5[2 * n2], f5[2 * n2 + 1], af, w);
+        }
+    }
+    for (int ii = wm; ii < WM; ++ii) {                          // H^T Q, F^T K
+        uint32_t ah[PX][4], af[PX][4];
+        const uint32_t ao = ((ii * 16 + (mi >> 1) * 8 + lr) * HP + wm * 16 + (mi & 1) * 8) * 2;
+#pragma unroll
+        for (int q = 0; q < PX; ++q) {
+            ldsm4t(ah[q], ht + q * GT * HP * 2 + ao);
+            ldsm4t(af[q], ft + q * GT * HP * 2 + ao);
+        }
+#pragma unroll
+        for (int n2 = 0; n2 < NBK / 2; ++n2) {
+            uint32_t w[PK][4];
+            const uint32_t bo = ((ii * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2;
+#pragma unroll
+            for (int q = 0; q < PK; ++q) ldsm4t(w[q], qt + q * GT * KP * 2 + bo);
+            add_product<PX, FX>(f5[2 * n2], f5[2 * n2 + 1], ah, w);
+#pragma unroll
+            for (int q = 0; q < PK; ++q) ldsm4t(w[q], kt + q * GT * KP * 2 + bo);
+            add_product<PX, FX>(f5[2 * n2], f5[2 * n2 + 1], af, w);
+        }
+    }
+    __syncthreads();
+    if (tid < left) {
+        float a = 0.f;
+        for (int w = 0; w < 8; ++w) a += dots[w];
+        a *= ga[GT - 1];
+        for (int j = 0; j < tid; ++j) a += su[j];
+        for (int i = tid; i < GT; ++i) a += gl[i];
+        reinterpret_cast<float*>(p.dG.p)[b * p.dG.bs + h * p.dG.hs + (tok + tid) * p.dG.ts] = a;
+        reinterpret_cast<float*>(p.dBeta.p)[b * p.dBeta.bs + h * p.dBeta.hs + (tok + tid) * p.dBeta.ts] = dbe[tid];
+    }
+#pragma unroll
+    for (int nb = 0; nb < NBK; ++nb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = i0 + 8 * half, col = wn * DKW + nb * 8 + 2 * t;
+            if (i >= left) continue;
+            const float q0 = fq[nb][2 * half], q1 = fq[nb][2 * half + 1], k0 = f5[nb][2 * half], k1 = f5[nb][2 * half + 1];
+            if (p.part) {
+                float* o = p.part + (bh * d.N + tok + i) * DK + col;
+                *reinterpret_cast<float2*>(o) = make_float2(q0, q1);
+                *reinterpret_cast<float2*>(o + (long long)d.B * d.h * d.N * DK) = make_float2(k0, k1);
+                continue;
+            }
+            const long long qo = b * p.dQ.bs + kh * p.dQ.hs + (tok + i) * p.dQ.ts + col, ko = b * p.dK.bs + kh * p.dK.hs + (tok + i) * p.dK.ts + col;
+            if constexpr (PK == 1) {
+                *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.dQ.p) + qo) = pack2(q0, q1);
+                *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.dK.p) + ko) = pack2(k0, k1);
+            } else {
+                *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.dQ.p) + qo) = make_float2(q0, q1);
+                *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.dK.p) + ko) = make_float2(k0, k1);
+            }
+        }
+}
+
+// dQ, dK [B][hk][N][dk] (strided views; half of the grid each) = the sums over the r value heads of a key head of the fp32
+// [B][h][N][dk] partial gradients, in head order.
+template <bool FP32>
+static __global__ void __launch_bounds__(256) sum_heads(const float* pq, const float* pk, View dQ, View dK, Dims d, long long n4) {
+    pdl_wait_primary();
+    const bool second = blockIdx.x >= gridDim.x / 2;
+    const long long x = (blockIdx.x - (second ? gridDim.x / 2 : 0)) * 256LL + threadIdx.x;
+    if (x >= n4) return;
+    const float* part = second ? pk : pq;
+    const View& out = second ? dK : dQ;
+    const int w4 = d.dk / 4, c = (int)(x % w4) * 4;
+    const long long row = x / w4;
+    const int t = (int)(row % d.N), kh = (int)(row / d.N % d.hk), b = (int)(row / d.N / d.hk);
+    if (t >= seq_len(d, b)) return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < d.r; ++r) {
+        const float4 v = *reinterpret_cast<const float4*>(part + (((long long)b * d.h + kh * d.r + r) * d.N + t) * d.dk + c);
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    }
+    const long long o = b * out.bs + kh * out.hs + t * out.ts + c;
+    if (FP32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(out.p) + o) = a;
+    else *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out.p) + o) = make_uint2(pack2(a.x, a.y), pack2(a.z, a.w));
 }
 
 // out = the sum over images of [B][n], in image order.
@@ -726,70 +755,17 @@ static ttt_status run_both(const Call& c, const Parts& Q, const Parts& K, const 
     return run_both_t<DK, P, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out, bo);
 }
 
-template <int DK, int P, int PK, bool GROUP>
-static ttt_status run_grads_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo) {
-    using L = GradsLayout<DK, P, PK>;
-    static_assert(L::smem <= 227 * 1024, "shared memory of a gradient CTA");
-    constexpr auto k = delta_grads<DK, P, PK, GROUP>;
-    ttt_status st = allow_smem<k>(L::smem);
-    if (st != TTT_OK) return st;
-    return launch(k, (long long)c.d.B * c.d.hk * c.d.ng, 256, L::smem, c.stream, c.d, Q, K, O, c.G, c.Beta, fo.E, bo.Y, fo.e_ps, fo.S, bo.D, c.dQ,
-                  c.dK, c.dG, c.dBeta);
-}
-
-#include "delta_grads_tc.cuh"
-
-// A strided bf16 token tensor with boxes of 64 tokens x rb bytes; false where it cannot be mapped.
-static bool map_tokens(CUtensorMap* m, const Parts& x, const Dims& d, int heads, int width, int rb, int* hmul, int* bmul) {
-    *hmul = x.hs != 0;
-    *bmul = x.bs != 0;
-    return encode_map(m, x.p, 2, {(cuuint64_t)width, (cuuint64_t)d.N, (cuuint64_t)(x.hs ? heads : 1), (cuuint64_t)(x.bs ? d.B : 1), 1},
-                      {x.ts ? x.ts : width, x.hs ? x.hs : width, x.bs ? x.bs : width, width}, rb, 64) &&
-           (x.ts != 0 || d.N == 1);
-}
-
-template <int DK>
-static ttt_status run_grads_tc(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo,
-                               float* part, bool* done) {
-    using L = GradsTc<DK>;
+// part: fp32 workspace of the gradients per value head, used where value heads share key heads.
+template <int DK, int PK>
+static ttt_status run_grads(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo, float* part) {
+    using L = GradsLayout<DK, PK>;
     const Dims& d = c.d;
-    GradsArgs a{};
-    const long long rows = (long long)d.B * d.h * d.N, srows = (long long)d.B * d.h * d.ng * 2 * d.dv;
-    *done = rows < (1LL << 31) - 64 && srows < (1LL << 31) - 64 &&
-            map_tokens(&a.K, K, d, d.hk, DK, 128, &a.kh, &a.kb) && map_tokens(&a.Q, Q, d, d.hk, DK, 128, &a.qh, &a.qb) &&
-            map_tokens(&a.O, O, d, d.h, d.dv, 64, &a.oh, &a.ob) &&
-            encode_map(&a.E, fo.E, 2, {(cuuint64_t)d.dv, (cuuint64_t)rows, 2, 1, 1}, {d.dv, fo.e_ps, fo.e_ps, fo.e_ps}, 64, 64) &&
-            encode_map(&a.Y, bo.Y, 2, {(cuuint64_t)d.dv, (cuuint64_t)rows, 2, 1, 1}, {d.dv, bo.y_ps, bo.y_ps, bo.y_ps}, 64, 64) &&
-            encode_map2(&a.S, fo.S, DK, srows, L::SV) && encode_map2(&a.D, bo.D, DK, srows, L::SV);
-    if (!*done) return TTT_OK;
-    a.d = d;
-    a.G = c.G; a.Beta = c.Beta; a.dG = c.dG; a.dBeta = c.dBeta;
-    a.dQ = c.dQ; a.dK = c.dK;
-    if (d.r > 1) {                             // fp32 sums per value head, then their sum
-        a.out_fp32 = a.out_per_head = 1;
-        a.dQ = View{reinterpret_cast<char*>(part), (long long)d.h * d.N * DK, (long long)d.N * DK, DK};
-        a.dK = View{reinterpret_cast<char*>(part + rows * DK), (long long)d.h * d.N * DK, (long long)d.N * DK, DK};
-    }
-    a.err = error_word(c);
-    a.wait_ns = c.wait_ns;
-    a.items = (long long)d.B * d.h * d.ng;
-    constexpr auto k = delta_grads_tc<DK>;
+    constexpr auto k = delta_grads<DK, PK>;
     ttt_status st = allow_smem<k>(L::smem);
     if (st != TTT_OK) return st;
-    st = launch(k, std::min<long long>(a.items, c.sms), 384, L::smem, c.stream, a);
+    const GradsArgs a{d, Q, K, O, c.G, c.Beta, fo.E, bo.Y, fo.e_ps, fo.S, bo.D, c.dQ, c.dK, c.dG, c.dBeta, d.r > 1 ? part : nullptr};
+    st = launch(k, (long long)d.B * d.h * d.ng, 256, L::smem, c.stream, a);
     if (st != TTT_OK || d.r == 1) return st;
-    const long long n4 = (long long)d.B * d.hk * d.N * DK / 4;
-    return launch(sum_heads, 2 * ((n4 + 255) / 256), 256, 0, c.stream, part, part + rows * DK, c.dQ, c.dK, d, n4);
-}
-
-template <int DK, int P, int PK>
-static ttt_status run_grads(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const ChainOut& fo, const BackOut& bo,
-                            float* part) {
-    if constexpr (PK == 1) {
-        bool done;
-        const ttt_status st = run_grads_tc<DK>(c, Q, K, O, fo, bo, part, &done);
-        if (done) return st;
-    }
-    // fp32 tokens, and token tensors that no tensor map describes (a token stride of zero)
-    return c.d.r > 1 ? run_grads_t<DK, P, PK, true>(c, Q, K, O, fo, bo) : run_grads_t<DK, P, PK, false>(c, Q, K, O, fo, bo);
+    const long long n4 = (long long)d.B * d.hk * d.N * DK / 4, rows = (long long)d.B * d.h * d.N;
+    return launch(sum_heads<PK == 3>, 2 * ((n4 + 255) / 256), 256, 0, c.stream, part, part + rows * DK, c.dQ, c.dK, d, n4);
 }

@@ -320,7 +320,9 @@ size_t ttt_gated_delta_workspace_bytes(int backward, const ttt_delta_shape* s);
  * Chunks of 32 tokens: inside a chunk the token updates are solved together (matrix products), the state
  * goes from chunk to chunk.  The state and all sums are fp32.  As operands of matrix instructions, bf16 tokens are exact and
  * everything else is carried as three bf16 parts (24 significant bits); but what ends in bf16 outputs alone (Z, dQ and dK of bf16
- * tokens) may be carried as two (16 bits).  Deterministic. */
+ * tokens) may be carried as two (16 bits).  Deterministic.
+ * A NaN or an infinity in token t's k, g or beta makes z of tokens t on and the last weights NaN, one in v_t (or W0) those of its feature,
+ * one in q_t z_t alone; what the recurrence gives before it is not touched. */
 ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,
                                    const ttt_view* Beta, const float* W0, int w0_shared, const int* lengths, float scale,
                                    const ttt_view* Z, float* W1_out, const ttt_delta_shape* s, void* ws, size_t ws_bytes,
@@ -334,7 +336,9 @@ ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const t
  *   dq_t = scale W_t^T dz_t,  dv_t = beta_t y_t,  dbeta_t = y_t . e_t,
  *   dk_t = beta_t (D_t^T e_t - e^{g_t} W_{t-1}^T y_t),
  *   dg_t = < e^{g_t} W_{t-1}, D_t - dv_t k_t^T >,   D_{t-1} = e^{g_t} (D_t - dv_t k_t^T) + scale dz_{t-1} q_{t-1}^T.
- * Rows of the gradients behind a sequence's length are left as they were.  Deterministic. */
+ * Rows of the gradients behind a sequence's length are left as they were.  Deterministic.
+ * Where a value of a sequence's tokens is not finite, the gradients of that sequence and its heads are not defined (those of
+ * other sequences are not touched). */
 ttt_status ttt_backward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,
                                     const ttt_view* Beta, const float* W0, int w0_shared, const int* lengths, float scale,
                                     const ttt_view* dZ, const float* dW1, const ttt_delta_shape* s, void* ws,

@@ -19,7 +19,8 @@
 // warp within a chunk, but for one: two warps share 16 rows, each with half of d_k, and add up their halves of K W^T through
 // shared memory (KS = 2).  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
 // take the readout and the stores, one chunk behind.  One warp for 16 rows against two: forward, 32 heads of 8192 tokens, d = 128,
-// 566 us against 439, 48 heads of 6084, d = 64, 288 against 285; backward, 32 heads of 4096, d = 128, 1190 against 1105.
+// 566 us against 439 (without the look for values that are not finite), 48 heads of 6084, d = 64, 288 against 285; backward, 32 heads of
+// 4096, d = 128, 1190 against 1105.
 //
 // Precision: W and all sums are fp32.  An operand of a matrix instruction that no bf16 value holds is split into bf16 parts,
 // products of parts below the last kept one dropped: PF = 3 parts (24 bits) wherever an fp32 result comes from it (W, R, T', suffix U; for fp32
@@ -29,9 +30,9 @@
 // products first or apart, and added to the rest in fp32.  2-norm errors, d = 64 .. 128, gates of 0 .. -3: W1 1 to 2e-7, fp32 Z 2e-7, gradients in fp32
 // 1 to 5e-7; a plain fp32 computation in chunks: 1 to 4e-7.  (Two parts for R and suffix U alone: W1 2.4e-6 and 2.6e-6.)
 //
-// Bound: the chain of chunks, about 2,950 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
+// Bound: the chain of chunks, about 3,200 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
 // multiply-adds per cycle and SM, about half of it; the rest is their latency and shared-memory reads of the token
-// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 52 us, chain 385 us.
+// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 52 us, chain 415 us.
 #include <algorithm>
 #include <array>
 #include <atomic>
@@ -192,6 +193,10 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
     }
     __syncwarp();
     const int g = lane >> 2, t = lane & 3;
+    // A row of L_21 that is not finite (or beyond bf16's range) must not reach the rows before it through the zeros of T_22: it
+    // counts as zero, and rows from the first one on are NaN.
+    auto beyond = [](float v) { return !(fabsf(v) < 3.39e38f); };
+    int bad = 32;
     uint32_t m[P][4];                              // T_22 L_21, its accumulators as the next left operand
     {
         uint32_t a[P][4];
@@ -210,8 +215,11 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
             for (int e = 0; e < 2; ++e) {
                 const int k = 16 + 2 * t + e * 8;
                 const float f0 = __shfl_sync(~0u, beta, U ? k : n * 8 + g), f1 = __shfl_sync(~0u, beta, U ? k + 1 : n * 8 + g);
+                float l0 = f0 * gm[k * GP + n * 8 + g], l1 = f1 * gm[(k + 1) * GP + n * 8 + g];
+                if (beyond(l1)) { bad = min(bad, k + 1); l1 = 0.f; }
+                if (beyond(l0)) { bad = min(bad, k); l0 = 0.f; }
                 uint32_t w[P];
-                split2<P>(f0 * gm[k * GP + n * 8 + g], f1 * gm[(k + 1) * GP + n * 8 + g], w);
+                split2<P>(l0, l1, w);
 #pragma unroll
                 for (int p = 0; p < P; ++p) b[p][e] = w[p];
             }
@@ -229,6 +237,7 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
             }
         }
     }
+    bad = __reduce_min_sync(~0u, bad);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         uint32_t b[P][2];
@@ -245,8 +254,9 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
         for (int pa = 0; pa < P; ++pa)
 #pragma unroll
             for (int pb = 0; pa + pb < P; ++pb) mma16816(c, m[pa], b[pb][0], b[pb][1]);
-        put_parts2<P>(image, 16 + g, n * 8 + 2 * t, -c[0], -c[1]);
-        put_parts2<P>(image, 24 + g, n * 8 + 2 * t, -c[2], -c[3]);
+        const float low = 16 + g >= bad ? __int_as_float(0x7fffffff) : 0.f, high = 24 + g >= bad ? __int_as_float(0x7fffffff) : 0.f;
+        put_parts2<P>(image, 16 + g, n * 8 + 2 * t, low - c[0], low - c[1]);
+        put_parts2<P>(image, 24 + g, n * 8 + 2 * t, high - c[2], high - c[3]);
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -430,6 +440,43 @@ __device__ __forceinline__ void as_operand(uint32_t (&a)[P][4], const float (&x)
     split2<P>(y[2], y[3], o);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][3] = o[p];
+}
+
+// A NaN or an infinity of one token must not reach the tokens before it, although a chunk's products meet it with zeros (0 x NaN is
+// NaN): where an operand's first parts show one (an infinity also stands for what bf16 cannot hold), such values count as zero, and results
+// from the first of a row on are NaN.  The look costs 469 against 440 us (forward, 32 heads of 8192 tokens, d = 128), nothing at d = 64.
+__device__ __forceinline__ bool not_finite(const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 z[2] = {zero, zero};                    // 0 x: NaN of what is not finite
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        z[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]), zero, z[0]);
+        z[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&b[i]), zero, z[1]);
+    }
+    z[0] = __hadd2(z[0], z[1]);
+    return __any_sync(~0u, (*reinterpret_cast<uint32_t*>(&z[0]) & 0x7fff7fffu) != 0);
+}
+// x: a [16 rows x 32 tokens] operand as four blocks of accumulators; first: the first hidden token of rows g and g + 8.
+__device__ __forceinline__ void hide_not_finite(float (&x)[4][4], int (&first)[2], int lane) {
+    first[0] = first[1] = CT;
+#pragma unroll
+    for (int nb = 3; nb >= 0; --nb)
+#pragma unroll
+        for (int q = 3; q >= 0; --q)
+            if (__float_as_uint(x[nb][q]) << 1 >= 0x7f7f8000u << 1) {      // what rounds beyond bf16's range
+                first[q >> 1] = nb * 8 + 2 * (lane & 3) + (q & 1);
+                x[nb][q] = 0.f;
+            }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) first[i] = min(first[i], __shfl_xor_sync(~0u, first[i], o));
+}
+// Block nb of results: NaN from the first hidden token of each row on.
+__device__ __forceinline__ void mark_hidden(float (&x)[4], const int (&first)[2], int nb, int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (nb * 8 + 2 * (lane & 3) + (q & 1) >= first[q >> 1]) x[q] = __int_as_float(0x7fffffff);
 }
 
 // A token tile in shared memory, as TMA writes it: [part][64-feature half][32 tokens][128 bytes], the 16-byte pieces
@@ -784,26 +831,35 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                     }
                     dot_tokens<DK, P, PK>(acc[0], acc[1], low[0], low[1], a, qt, z, kk, lane);
                 }
+                float e[4][4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    const float4 v = lds4(ep + (nb * 32 + lane) * 16);
+                    const float2 be = lds2(gt + (2 * CT + nb * 8 + 2 * t) * 4);
+                    e[nb][0] = be.x * v.x; e[nb][1] = be.y * v.y; e[nb][2] = be.x * v.z; e[nb][3] = be.y * v.w;
+                }
                 uint32_t u[2][P][4];
+                as_operand<P>(u[0], e[0], e[1]);
+                as_operand<P>(u[1], e[2], e[3]);
+                int first[2];
+                const bool hidden = not_finite(u[0][0], u[1][0]);
+                if (hidden) {
+                    hide_not_finite(e, first, lane);
+                    as_operand<P>(u[0], e[0], e[1]);
+                    as_operand<P>(u[1], e[2], e[3]);
+                }
+                float au[2][4] = {};
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    float e[2][4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 v = lds4(ep + ((2 * kk + i) * 32 + lane) * 16);
-                        const float2 be = lds2(gt + (2 * CT + (2 * kk + i) * 8 + 2 * t) * 4);
-                        e[i][0] = be.x * v.x; e[i][1] = be.y * v.y; e[i][2] = be.x * v.z; e[i][3] = be.y * v.w;
-                    }
-                    as_operand<P>(u[kk], e[0], e[1]);
+                for (int i = 0; i < 2; ++i) {
+                    mat_block<P, P, true>(au[i], u, am, 2 * z + i, lane);
+                    if (hidden) mark_hidden(au[i], first, 2 * z + i, lane);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int nb = 2 * z + i;
                     const float2 ga = lds2(gt + (nb * 8 + 2 * t) * 4);
-                    float au[4] = {};
-                    mat_block<P, P, true>(au, u, am, nb, lane);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(d.scale * ((q & 1) ? ga.y : ga.x), acc[i][q] + low[i][q], au[q]);
+                    for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(d.scale * ((q & 1) ? ga.y : ga.x), acc[i][q] + low[i][q], au[i][q]);
                 }
                 put_pair_tokens<PK>(stagebuf, acc[0], acc[1], out.Z.p,
                                     b * out.Z.bs + h * out.Z.hs + ((long long)pc * CT + z * 16) * out.Z.ts + row0, out.Z.ts, left - z * 16, lane);
@@ -880,8 +936,18 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
         uint32_t a[2][PF][4];
         as_operand<PF>(a[0], x[0], x[1]);
         as_operand<PF>(a[1], x[2], x[3]);
+        int first[2];
+        const bool hidden = not_finite(a[0][0], a[1][0]);
+        if (hidden) {
+            hide_not_finite(x, first, lane);
+            as_operand<PF>(a[0], x[0], x[1]);
+            as_operand<PF>(a[1], x[2], x[3]);
+        }
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) mat_block<PF, PF, true>(e[nb], a, tm, nb, lane);
+        if (hidden)
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) mark_hidden(e[nb], first, nb, lane);
         // W <- gamma_C W + (suffix beta E)^T K
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {

@@ -9,6 +9,10 @@ other strides the library accepts, so tensors laid out by token ([B][N][heads][d
 
 Unlike the full-batch heads' calls, these allocate their workspace for the call (torch's allocator orders its
 reuse on the call's stream), so calls on several streams and captured graphs share nothing.
+
+A device-side wait that runs out (a copy that does not come within a second) leaves outputs unwritten and is recorded in the
+call's workspace only.  A caller who wants to know passes a workspace (``gated_delta_workspace``) and reads it with
+``workspace_status`` after the call.
 """
 import torch
 
@@ -76,12 +80,24 @@ def _workspace(backward, Q, V):
     return torch.empty(n, dtype=torch.uint8, device=Q.device) if n else None      # 0: the call itself reports why
 
 
+def gated_delta_workspace(Q, V, backward=False):
+    """A workspace for forward_gated_delta (backward: backward_gated_delta) on tensors of these shapes and type, to pass as `ws`.
+    Calls that may run at the same time need distinct ones.  ``workspace_status(ws)`` waits for the stream and tells
+    whether a device-side wait of the last call on it ran out."""
+    with _On(Q, None):
+        ws = _workspace(backward, Q, V)
+    if ws is None:
+        raise ValueError("no such gated delta shape (d_k and d_v are 64 or 128)")
+    return ws
+
+
 def forward_gated_delta(Q, K, V, G, Beta, W0=None, lengths=None, scale=1.0, Z=None, W1_out=None, ws=None, stream=None):
     """The gated delta rule over whole sequences: per value head, from W0,
         W_t = exp(g_t) W_{t-1} + beta_t (v_t - exp(g_t) W_{t-1} k_t) k_t^T,   z_t = scale W_t q_t.
     W0: None (zeros), [heads][d_v][d_k] fp32 shared by the batch, or [B][heads][d_v][d_k].  lengths: None or
     [B] int32: the tokens of each sequence; rows of Z behind them are left as they were (zeros in a Z
-    allocated here).  W1_out (optional, [B][heads][d_v][d_k] fp32) receives the last weights.  Returns Z."""
+    allocated here).  W1_out (optional, [B][heads][d_v][d_k] fp32) receives the last weights.  ws: None (allocated for the call), or
+    a gated_delta_workspace, whose status tells of a device-side wait that ran out.  Returns Z."""
     with _On(Q, stream) as st:
         if ws is None:
             ws = _workspace(False, Q, V)
@@ -96,7 +112,7 @@ def backward_gated_delta(Q, K, V, G, Beta, dZ, W0=None, dW1=None, lengths=None, 
     weights.  Returns (dQ, dK, dV, dG, dBeta, dW0): dQ and dK summed over the value heads that share a key
     head, dW0 like W0 (None without one; a shared W0's is summed over the batch).  `out` may supply those
     six tensors (dW0 None: not wanted); rows behind a sequence's length are left as they were there, and
-    zeros otherwise."""
+    zeros otherwise.  ws as in forward_gated_delta (with backward=True)."""
     with _On(Q, stream) as st:
         if ws is None:
             ws = _workspace(True, Q, V)

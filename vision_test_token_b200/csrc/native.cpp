@@ -204,6 +204,19 @@ PyObject* workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// Whether the elements of a [B][heads][N] or [B][heads][N][d] tensor lie in the order of [B][N][heads][d], without gaps.
+bool by_token(const at::Tensor& t) {
+    const int64_t n = t.dim();
+    if (n != 3 && n != 4) return false;
+    int64_t step = 1;
+    for (int64_t i : {(int64_t)3, (int64_t)1, (int64_t)2, (int64_t)0}) {       // from the innermost
+        if (i >= n) continue;
+        if (t.size(i) != 1 && t.stride(i) != step) return false;
+        step *= t.size(i);
+    }
+    return true;
+}
+
 // clip(grads, out or None, max_norm, norm, ws, stream); grads, out: lists or tuples
 PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 6, [&]() -> long {
@@ -220,7 +233,8 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!device.is_cuda()) throw Refused{"gradients must be CUDA tensors"};
         for (Py_ssize_t i = 0; i < m; ++i) {
             const at::Tensor& g = tensor(PySequence_Fast_GET_ITEM(a[0], i), "gradient");
-            if (g.device() != device || !g.is_contiguous()) throw Refused{"gradients must be contiguous tensors on one device"};
+            const bool plain = g.is_contiguous(), tokens = by_token(g);
+            if (g.device() != device || (!plain && !tokens)) throw Refused{"gradients must be tensors on one device, contiguous or laid out by token"};
             if (g.scalar_type() == at::kBFloat16) types[i] = TTT_BF16;
             else if (g.scalar_type() == at::kFloat) types[i] = TTT_FP32;
             else throw Refused{"gradients must be bfloat16 or float32"};
@@ -228,8 +242,9 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
             counts[i] = g.numel();
             if (a[1] != Py_None) {
                 const at::Tensor& o = tensor(PySequence_Fast_GET_ITEM(a[1], i), "output");
-                if (o.sizes() != g.sizes() || o.scalar_type() != g.scalar_type() || o.device() != device || !o.is_contiguous())
-                    throw Refused{"outputs must be contiguous and like their gradients"};
+                if (o.sizes() != g.sizes() || o.scalar_type() != g.scalar_type() || o.device() != device ||
+                    !((plain && o.is_contiguous()) || (tokens && by_token(o))))
+                    throw Refused{"outputs must be like their gradients and laid out like them"};
                 out[i] = o.data_ptr();
             }
         }

@@ -138,8 +138,9 @@ def step_gated_delta(Q, K, V, G, Beta, W, slots=None, scale=1.0, Z=None, stream=
 
 
 def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
-    """Scales the gradients (bf16 or fp32 CUDA tensors, contiguous) by min(1, max_norm / norm), norm the
-    2-norm over all their elements: in place, or into the tensors of `out` (same shapes and dtypes).
+    """Scales the gradients (bf16 or fp32 CUDA tensors, contiguous, or laid out by token as the gradients of
+    backward_gated_delta are for such inputs: x.transpose(1, 2) is contiguous) by min(1, max_norm / norm), norm the
+    2-norm over all their elements: in place, or into the tensors of `out` (same shapes, dtypes and layouts).
     Returns the norm before clipping, a 1-element fp32 tensor; nothing waits for the GPU."""
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)

@@ -42,3 +42,20 @@ def test_workspace_refusals(cuda_dev):
     ws = gated_delta_workspace(y["Q"], y["V"])
     with pytest.raises(RuntimeError, match="WORKSPACE"):          # a forward call's is too small for the backward pass
         backward_gated_delta(*(y[n] for n in INPUTS), y["dZ"], ws=ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("backward", [False, True])
+def test_empty_sequences_leave_the_workspace_alone(cuda_dev, dtype, backward):
+    """Nothing behind a sequence's end is read: a batch of empty sequences makes nothing of its tokens in the workspace."""
+    y = _on(_make(2, 1, 2, 100, 64, 64, dtype, w0="none", seed=52), cuda_dev)
+    args = [y[n] for n in INPUTS]
+    ws = gated_delta_workspace(y["Q"], y["V"], backward=backward)
+    ws.fill_(0xA5)
+    lengths = torch.tensor([0, -3], dtype=torch.int32, device=cuda_dev)
+    if backward:
+        backward_gated_delta(*args, y["dZ"], lengths=lengths, ws=ws)
+    else:
+        forward_gated_delta(*args, lengths=lengths, ws=ws)
+    torch.cuda.synchronize()
+    assert (ws[256:] == 0xA5).all()                               # the header holds the status

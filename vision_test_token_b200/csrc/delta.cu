@@ -50,7 +50,7 @@ struct SplitArgs {
     __nv_bfloat16* out[3];
     long long ps[3];                  // elements of a tensor = part stride
     int heads[3], width[3];
-    int N;
+    Dims d;
 };
 template <int P>
 __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ SplitArgs a) {
@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ Spli
     for (long long x = blockIdx.x * 256LL + threadIdx.x; x < total; x += gridDim.x * 256LL) {
         const int c = (int)(x % w4) * 4;
         const long long row = x / w4;
-        const int bh = (int)(row / a.N), t = (int)(row - (long long)bh * a.N), b = bh / heads, h = bh - b * heads;
+        const int bh = (int)(row / a.d.N), t = (int)(row - (long long)bh * a.d.N), b = bh / heads, h = bh - b * heads;
+        if (t >= seq_len(a.d, b)) continue;            // what lies behind a sequence is not read
         const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x[i].p) + b * a.x[i].bs + h * a.x[i].hs +
                                                           t * a.x[i].ts + c);
         uint32_t lo[P], hi[P];
@@ -1117,7 +1118,7 @@ struct Splitter {
     }
     ttt_status run() {
         if (!n) return TTT_OK;
-        a.N = c.d.N;
+        a.d = c.d;
         long long most = 0;
         for (int i = 0; i < n; ++i) most = std::max(most, a.ps[i]);
         split_tokens<3><<<dim3((unsigned)std::min<long long>((most / 4 + 255) / 256, 148 * 8), n), 256, 0, c.stream>>>(a);

@@ -1121,7 +1121,7 @@ struct Splitter {
         a.d = c.d;
         long long most = 0;
         for (int i = 0; i < n; ++i) most = std::max(most, a.ps[i]);
-        split_tokens<3><<<dim3((unsigned)std::min<long long>((most / 4 + 255) / 256, 148 * 8), n), 256, 0, c.stream>>>(a);
+        split_tokens<3><<<dim3((unsigned)std::min<long long>((most / 4 + 255) / 256, 8LL * c.sms), n), 256, 0, c.stream>>>(a);
         return check_launch(cudaGetLastError());
     }
 };

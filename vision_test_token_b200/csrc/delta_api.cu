@@ -284,6 +284,7 @@ ttt_status ttt_step_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_
     k.flat(W, (long long)n_slots * s->heads * s->d_v * s->d_k * 4, true);
     st = k.finish();
     if (st != TTT_OK) return st;
+    c.sms = sm_count();
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_step(c, W, slots, n_slots);
 }

@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(128) delta_step(StepArgs s) {
 }
 
 template <typename E, int DK>
-static ttt_status step_t(const StepArgs& s, cudaStream_t st) {
+static ttt_status step_t(const StepArgs& s, int sms, cudaStream_t st) {
     const long long rows = (long long)s.d.B * s.d.h * s.d.dv;
     // One row per thread spreads a small batch over more SMs, four have more loads in flight.  Heads of 128 x 128, one
     // row against four: 32 heads 2.5 / 2.7 us, 512 heads 13.3 / 13.4, 1024 heads 24.6 / 23.8, 8192 heads 225 / 161.
-    if (rows >= 64LL * 148 * 8)
+    if (rows >= 512LL * sms)
         delta_step<E, DK, 4><<<(unsigned)(rows / 64), 128, 0, st>>>(s);
     else
         delta_step<E, DK, 1><<<(unsigned)(rows / 16), 128, 0, st>>>(s);
@@ -154,8 +154,8 @@ static ttt_status step_t(const StepArgs& s, cudaStream_t st) {
 
 ttt_status launch_step(const Call& c, float* W, const int* slots, int n_slots) {
     const StepArgs s{c.d, c.Q, c.K, c.V, c.G, c.Beta, c.Z, W, slots, n_slots};
-    if (c.fp32) return c.d.dk == 64 ? step_t<float, 64>(s, c.stream) : step_t<float, 128>(s, c.stream);
-    return c.d.dk == 64 ? step_t<__nv_bfloat16, 64>(s, c.stream) : step_t<__nv_bfloat16, 128>(s, c.stream);
+    if (c.fp32) return c.d.dk == 64 ? step_t<float, 64>(s, c.sms, c.stream) : step_t<float, 128>(s, c.sms, c.stream);
+    return c.d.dk == 64 ? step_t<__nv_bfloat16, 64>(s, c.sms, c.stream) : step_t<__nv_bfloat16, 128>(s, c.sms, c.stream);
 }
 
 }  // namespace gd

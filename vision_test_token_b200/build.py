@@ -6,8 +6,10 @@ Every .cu file under csrc/ is compiled with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and linked, with the static CUDA runtime,
 into ``vision_test_token_b200/libttt.so``.  No torch headers or libraries are involved in that.
 csrc/native.cpp (the fast marshalling of torch tensors for the per-token entries) is compiled with g++ against
-torch's headers into ``vision_test_token_b200/_native.so``, which links to libttt.so.
+torch's headers into ``vision_test_token_b200/_native.so``, which links to libttt.so.  It is built again when torch or Python is
+another one, and left out, with a note, where there is no torch: libttt.so serves C callers without it.
 """
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -21,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libttt.so")
 NATIVE = os.path.join(PKG, "_native.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+NATIVE_KEY = os.path.join(BUILD_DIR, "native.key")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -35,16 +38,47 @@ def _sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "ttt.h")]
-    return [f for f in files if os.path.isfile(f)]
+def _newest(files):
+    return max(os.path.getmtime(f) for f in files)
+
+
+def _lib_deps():
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
+    return files + [os.path.join(INCLUDE, "ttt.h")]
+
+
+def _native_key():
+    """What _native.so is built for besides its sources; None without torch (found without the slow import of it)."""
+    try:
+        return f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _native_is_current(key):
+    if not os.path.exists(NATIVE) or not os.path.exists(NATIVE_KEY):
+        return False
+    with open(NATIVE_KEY) as f:
+        if f.read() != key:
+            return False
+    return os.path.getmtime(NATIVE) >= _newest([os.path.join(CSRC, "native.cpp"), os.path.join(INCLUDE, "ttt.h")])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(OUT) and os.path.exists(NATIVE):
-        newest = max(os.path.getmtime(f) for f in _deps())
-        if min(os.path.getmtime(OUT), os.path.getmtime(NATIVE)) >= newest:
-            return OUT
+    if force or not os.path.exists(OUT) or os.path.getmtime(OUT) < _newest(_lib_deps()):
+        _build_lib(verbose)
+    key = _native_key()
+    if key is None:
+        sys.stderr.write("no torch here: libttt.so is built, its binding for torch tensors (_native.so) is not\n")
+    elif force or not _native_is_current(key):
+        _build_native()
+        os.makedirs(os.path.dirname(NATIVE_KEY), exist_ok=True)
+        with open(NATIVE_KEY, "w") as f:
+            f.write(key)
+    return OUT
+
+
+def _build_lib(verbose):
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -69,8 +103,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = OUT + ".tmp"
     subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], check=True)
     os.replace(tmp, OUT)
-    _build_native()
-    return OUT
 
 
 def _build_native():

@@ -290,7 +290,7 @@ ttt_status ttt_backward_mlp(const void* Q, const void* K, const void* V, const f
  * cut out of a larger projection are all passed as they are.
  *   Q, K: qk_heads heads of width d_k;  V, Z: heads heads of width d_v, dtype (bf16 or fp32).  Value head h
  *   uses key head h / (heads / qk_heads); heads is a multiple of qk_heads.  d_k, d_v: 64 or 128.
- *   G (log of the gate, normally <= 0; -inf drops the state), Beta: fp32, one value per token and value
+ *   G (log of the gate, normally <= 0; -inf drops the state, a finite one), Beta: fp32, one value per token and value
  *   head (width 1).
  * Base pointers and strides of the token tensors are multiples of 16 bytes (strides of dimensions of
  * size 1 are ignored).  Everything lies on the current device.  Inputs may be broadcast (stride 0) and may share

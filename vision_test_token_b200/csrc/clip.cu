@@ -1,14 +1,15 @@
 // clip.cu -- the global norm of many tensors and their scaling to a largest norm:
 //   n = sqrt(sum over all tensors of x^2),   out = x min(1, max_norm / n).
 //
-// Two launches whatever the number of tensors (up to kTable per launch): the first reads every tensor once and
+// Two launches for up to kTable tensors (two more for each kTable beyond): the first reads every tensor once and
 // leaves one partial sum per CTA, the second starts by adding those up (the same order in every CTA, so
 // that all use the same factor) and scales.  The tensors' addresses travel as a kernel argument, so that
 // nothing is copied to the device and a captured graph holds all it needs.
 //
 // Bound: HBM, one read for the norm, then one read and one write.  The second pass walks the tensors backwards:
 // what the first read last is still in L2 (126 MB) and is read from there.  667 MB of bf16 and fp32 gradients in 60
-// tensors: 337 us, 5.9 TB/s counting both reads.  60 tensors of 400,000 elements in all: 27 us, the two launches.  Sums: fp32 over the 4 or 8
+// tensors: 338 to 350 us, 5.8 TB/s counting both reads.  60 tensors of 400,000 elements in all: 25 us, the host's (its checks of each
+// tensor and two launches).  Sums: fp32 over the 4 or 8
 // values of a 16-byte piece (fp64 where their squares leave fp32's range), then fp64; fixed order.
 #include <algorithm>
 
@@ -22,7 +23,8 @@ constexpr int kSmall = 64;
 constexpr int kThreads = 256;
 constexpr int kLoads = 8;                 // 16-byte loads a thread has in flight
 constexpr int kPiece = kThreads * 16 * kLoads;   // bytes of a tensor that a CTA takes at a time
-constexpr int kMaxCtas = 148 * 32;         // several waves: 377 us with as many CTAs as fit at a time, 341 us with these (667 MB of gradients)
+// 32 for each of a B200's SMs, several waves: 377 us with as many as fit at a time, 341 us with these (667 MB of gradients).  Sizes the workspace.
+constexpr int kMaxCtas = 148 * 32;
 
 struct Item {
     const char* in;

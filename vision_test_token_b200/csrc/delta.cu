@@ -1026,7 +1026,7 @@ static Tiled tiled(const Parts& x, int parts, const Dims& d, int heads, int widt
 }
 
 // Launches `k` as a programmatic dependent of what precedes it in the stream: its set-up overlaps that kernel's tail.
-// (Every kernel here waits for its predecessor before it reads or writes global memory.)
+// (Every kernel here waits for its predecessor before it reads or writes global memory.  split_tokens and the step are plain launches.)
 template <class... P, class... A>
 static ttt_status launch(void (*k)(P...), long long grid, int threads, int smem, cudaStream_t st, A... args) {
     cudaLaunchAttribute attr{};

@@ -319,8 +319,7 @@ size_t ttt_gated_delta_workspace_bytes(int backward, const ttt_delta_shape* s);
  * after each sequence's last token.
  * Chunks of 32 tokens: inside a chunk the token updates are solved together (matrix products), the state
  * goes from chunk to chunk.  The state and all sums are fp32.  As operands of matrix instructions, bf16 tokens are exact and
- * everything else is carried as three bf16 parts (24 significant bits); but what ends in bf16 outputs alone (Z, dQ and dK of bf16
- * tokens) may be carried as two (16 bits).  Deterministic.
+ * everything else is carried as three bf16 parts (24 significant bits).  Deterministic.
  * A NaN or an infinity in token t's k, g or beta makes z of tokens t on and the last weights NaN, one in v_t (or W0) those of its feature,
  * one in q_t z_t alone; what the recurrence gives before it is not touched. */
 ttt_status ttt_forward_gated_delta(const ttt_view* Q, const ttt_view* K, const ttt_view* V, const ttt_view* G,

@@ -19,20 +19,18 @@
 // warp within a chunk, but for one: two warps share 16 rows, each with half of d_k, and add up their halves of K W^T through
 // shared memory (KS = 2).  A loader warp brings the token tiles by TMA a chunk or two ahead, and helper warps
 // take the readout and the stores, one chunk behind.  One warp for 16 rows against two: forward, 32 heads of 8192 tokens, d = 128,
-// 566 us against 439 (without the look for values that are not finite), 48 heads of 6084, d = 64, 288 against 285; backward, 32 heads of
-// 4096, d = 128, 1190 against 1105.
+// 638 us against 488, 48 heads of 6084, d = 64, 337 against 297; backward, 32 heads of 4096, d = 128, 1224 against 1070.
 //
-// Precision: W and all sums are fp32.  An operand of a matrix instruction that no bf16 value holds is split into bf16 parts,
-// products of parts below the last kept one dropped: PF = 3 parts (24 bits) wherever an fp32 result comes from it (W, R, T', suffix U; for fp32
-// tokens, themselves split by a pass of their own, all of them), two in the readout of bf16 tokens (W, U, A), whose Z is rounded to
-// eight bits anyway.  The matrix instructions truncate: each of an instruction's products is cut at a quarter of the last place of the
-// largest addend, and the sum towards zero.  So sums of many products are taken in accumulators of their own, the small
-// products first or apart, and added to the rest in fp32.  2-norm errors, d = 64 .. 128, gates of 0 .. -3: W1 1 to 2e-7, fp32 Z 2e-7, gradients in fp32
-// 1 to 5e-7; a plain fp32 computation in chunks: 1 to 4e-7.  (Two parts for R and suffix U alone: W1 2.4e-6 and 2.6e-6.)
+// Precision: W and all sums are fp32.  An operand of a matrix instruction that no bf16 value holds (W, R, E, U, T', A; fp32 tokens, by a
+// pass of their own) is split into three bf16 parts, 24 bits, products of parts below the third dropped.  The matrix instructions
+// truncate: each of an instruction's products is cut at a quarter of the last place of the largest addend, and the sum towards zero.
+// So sums of many products are taken in accumulators of their own, the small products first or apart, and added to the rest in fp32.
+// 2-norm errors, d = 64 .. 128, gates of 0 .. -3: W1 1 to 2e-7, fp32 Z 2e-7, gradients in fp32 1 to 5e-7; a plain fp32 computation in
+// chunks: 1 to 4e-7.  (Two parts for R or suffix U alone: W1 2.4e-6, 2.6e-6; two in the readout, 5 to 10 % faster: Z 3e-6 before its rounding.)
 //
-// Bound: the chain of chunks, about 3,200 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
+// Bound: the chain of chunks, about 3,300 cycles for 32 tokens at d = 128 (matrix instructions, measured at 1,009
 // multiply-adds per cycle and SM, about half of it; the rest is their latency and shared-memory reads of the token
-// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 52 us, chain 415 us.
+// operands).  32 heads of 8192 tokens, d = 128, two value heads to a key head: prep 55 us, chain 435 us.
 #include <algorithm>
 #include <array>
 #include <atomic>
@@ -52,7 +50,6 @@ struct SplitArgs {
     int heads[3], width[3];
     Dims d;
 };
-template <int P>
 __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ SplitArgs a) {
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -66,8 +63,8 @@ __global__ void __launch_bounds__(256) split_tokens(const __grid_constant__ Spli
         const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x[i].p) + b * a.x[i].bs + h * a.x[i].hs +
                                                           t * a.x[i].ts + c);
         uint32_t lo[P], hi[P];
-        split2<P>(v.x, v.y, lo);
-        split2<P>(v.z, v.w, hi);
+        split2(v.x, v.y, lo);
+        split2(v.z, v.w, hi);
 #pragma unroll
         for (int p = 0; p < P; ++p) *reinterpret_cast<uint2*>(a.out[i] + p * a.ps[i] + row * a.width[i] + c) = make_uint2(lo[p], hi[p]);
     }
@@ -82,7 +79,7 @@ constexpr int GP = CT + 4;            // row pitch (floats) of the 32 x 32 fp32 
 // Shared memory (59 KB a CTA) keeps three CTAs, twelve warps, on an SM.
 constexpr int kPrepWarps = 4;
 // A warp's shared memory: Gamma, then G in its place, one matrix image, and two 16 x 16 blocks.
-constexpr int kPrepWarpBytes = CT * GP * 4 + mat_bytes(PF) + 2 * 16 * 20 * 4;
+constexpr int kPrepWarpBytes = CT * GP * 4 + kMat + 2 * 16 * 20 * 4;
 
 // The lower triangles of K K^T (c) and Q K^T (w) of 32 tokens, rows behind `left` as zeros.  The operands go from global
 // memory to registers: any order of the features does as long as both sides have it, so that a lane takes 8
@@ -142,33 +139,26 @@ __device__ __forceinline__ void gram32(float (&c)[2][4][4], float (&w)[2][4][4],
 }
 
 // Elements (i, j) and (i, j + 1), j even, of a bf16 part image.
-template <int P>
 __device__ __forceinline__ void put_parts2(uint8_t* mat, int i, int j, float x, float y) {
     uint32_t w[P];
-    split2<P>(x, y, w);
+    split2(x, y, w);
 #pragma unroll
     for (int p = 0; p < P; ++p) *reinterpret_cast<uint32_t*>(mat + ((p * CT + i) * MP + j) * 2) = w[p];
 }
 
 // The warp's matrix image in shared memory -> global memory.
-template <int P>
 __device__ __forceinline__ void copy_image(uint8_t* dst, const uint8_t* image, int lane) {
     __syncwarp();
 #pragma unroll
-    for (int x = lane; x < mat_bytes(P) / 16; x += 32) reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(image)[x];
+    for (int x = lane; x < kMat / 16; x += 32) reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(image)[x];
     __syncwarp();
-}
-// Zeros in the 16 x 16 block above the diagonal blocks of an image's last part.
-template <int P>
-__device__ __forceinline__ void zero_upper(uint8_t* image, int lane) {
-    *reinterpret_cast<uint4*>(image + (((P - 1) * CT + (lane >> 1)) * MP + 16 + (lane & 1) * 8) * 2) = make_uint4(0, 0, 0, 0);
 }
 constexpr int XP = 20, kBlock = 16 * XP;   // row pitch and size (floats) of a 16 x 16 block
 
 // The image of (I + G diag(beta))^{-1} (U: of (I + diag(beta) G)^{-1}), G 32 x 32, strictly lower triangular.  The two 16 x 16
 // blocks on the diagonal are inverted by forward substitution, a column per lane; the block below them is
 // - T_22 L_21 T_11 on matrix instructions, whose operands are P parts as the image's elements are.
-template <int P, bool U>
+template <bool U>
 __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, float* blocks, float beta, int lane) {
     {
         const int half = lane >> 4, col = lane & 15;
@@ -205,7 +195,7 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
         for (int e = 0; e < 4; ++e) {
             const float2 v = *reinterpret_cast<const float2*>(blocks + kBlock + (g + (e & 1) * 8) * XP + 2 * t + (e >> 1) * 8);
             uint32_t w[P];
-            split2<P>(v.x, v.y, w);
+            split2(v.x, v.y, w);
 #pragma unroll
             for (int p = 0; p < P; ++p) a[p][e] = w[p];
         }
@@ -220,7 +210,7 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
                 if (beyond(l1)) { bad = min(bad, k + 1); l1 = 0.f; }
                 if (beyond(l0)) { bad = min(bad, k); l0 = 0.f; }
                 uint32_t w[P];
-                split2<P>(l0, l1, w);
+                split2(l0, l1, w);
 #pragma unroll
                 for (int p = 0; p < P; ++p) b[p][e] = w[p];
             }
@@ -232,7 +222,7 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t w[P];
-                split2<P>(c[2 * e], c[2 * e + 1], w);
+                split2(c[2 * e], c[2 * e + 1], w);
 #pragma unroll
                 for (int p = 0; p < P; ++p) m[p][2 * n + e] = w[p];
             }
@@ -246,7 +236,7 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
         for (int e = 0; e < 2; ++e) {
             const float* x = blocks + (2 * t + e * 8) * XP + n * 8 + g;
             uint32_t w[P];
-            split2<P>(x[0], x[XP], w);
+            split2(x[0], x[XP], w);
 #pragma unroll
             for (int p = 0; p < P; ++p) b[p][e] = w[p];
         }
@@ -256,18 +246,18 @@ __device__ __forceinline__ void inverse_image(uint8_t* image, const float* gm, f
 #pragma unroll
             for (int pb = 0; pa + pb < P; ++pb) mma16816(c, m[pa], b[pb][0], b[pb][1]);
         const float low = 16 + g >= bad ? __int_as_float(0x7fffffff) : 0.f, high = 24 + g >= bad ? __int_as_float(0x7fffffff) : 0.f;
-        put_parts2<P>(image, 16 + g, n * 8 + 2 * t, low - c[0], low - c[1]);
-        put_parts2<P>(image, 24 + g, n * 8 + 2 * t, high - c[2], high - c[3]);
+        put_parts2(image, 16 + g, n * 8 + 2 * t, low - c[0], low - c[1]);
+        put_parts2(image, 24 + g, n * 8 + 2 * t, high - c[2], high - c[3]);
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
         const int block = r >> 2, i = (r & 3) * 4 + (lane >> 3), j = (lane & 7) * 2;
         const float2 v = *reinterpret_cast<const float2*>(blocks + block * kBlock + i * XP + j);
-        put_parts2<P>(image, block * 16 + i, block * 16 + j, v.x, v.y);
+        put_parts2(image, block * 16 + i, block * 16 + j, v.x, v.y);
     }
 }
 
-template <int DK, int P, int PK, bool BACKWARD>
+template <int DK, int PK, bool BACKWARD>
 __global__ void __launch_bounds__(kPrepWarps * 32, PK == 1 ? 3 : 2)
 delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long total, uint32_t* err) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -285,7 +275,7 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
     uint8_t* my = smem + warp * kPrepWarpBytes;
     float* kkm = reinterpret_cast<float*>(my);
     uint8_t* image = my + CT * GP * 4;
-    float* blocks = reinterpret_cast<float*>(image + mat_bytes(PF));
+    float* blocks = reinterpret_cast<float*>(image + kMat);
     // gates of token `lane`; tokens past the end of the sequence neither fade nor write
     const long long t = (long long)c * CT + lane;
     const bool live = lane < left;
@@ -299,7 +289,7 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
         if (lane >= o) pre += a;
         if (lane + o < 32) suf += z;
     }
-    uint8_t* out = rec + item * rec_bytes(P, BACKWARD);
+    uint8_t* out = rec + item * rec_bytes(BACKWARD);
     float* gates = reinterpret_cast<float*>(out);
     gates[lane] = expf(pre);
     gates[CT + lane] = expf(suf);
@@ -328,24 +318,23 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
                 for (int e = 0; e < 2; ++e) {
                     const int i = x * 16 + (lane >> 2) + e * 8, j = n * 8 + 2 * (lane & 3);
                     if (n > 2 * x + 1) {                       // above the diagonal (G is zero there already)
-                        put_parts2<P>(image, i, j, 0.f, 0.f);
+                        put_parts2(image, i, j, 0.f, 0.f);
                         continue;
                     }
                     const bool edge = n >= 2 * x;              // the diagonal may pass: nothing above it may come through, NaN neither
                     float2* dec = reinterpret_cast<float2*>(kkm + i * GP + j);
                     const float2 gm = *dec;
-                    put_parts2<P>(image, i, j, edge && j > i ? 0.f : d.scale * gm.x * w[x][n][2 * e],
+                    put_parts2(image, i, j, edge && j > i ? 0.f : d.scale * gm.x * w[x][n][2 * e],
                                   edge && j + 1 > i ? 0.f : d.scale * gm.y * w[x][n][2 * e + 1]);
                     *dec = make_float2(edge && j >= i ? 0.f : gm.x * m[x][n][2 * e], edge && j + 1 >= i ? 0.f : gm.y * m[x][n][2 * e + 1]);
                 }
     }
-    copy_image<P>(out + kRecA, image, lane);
-    if (P < PF) zero_upper<PF>(image, lane);
-    inverse_image<PF, false>(image, kkm, blocks, beta, lane);  // what lies above the diagonal is zero from A on
-    copy_image<PF>(out + kGateBytes, image, lane);
+    copy_image(out + kGateBytes + kMat, image, lane);
+    inverse_image<false>(image, kkm, blocks, beta, lane);  // what lies above the diagonal is zero from A on
+    copy_image(out + kGateBytes, image, lane);
     if constexpr (BACKWARD) {
-        inverse_image<PF, true>(image, kkm, blocks, beta, lane);
-        copy_image<PF>(out + kRecA + mat_bytes(P), image, lane);
+        inverse_image<true>(image, kkm, blocks, beta, lane);
+        copy_image(out + kGateBytes + 2 * kMat, image, lane);
     }
 }
 
@@ -354,7 +343,7 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
 // --------------------------------------------------------------------------------------------------
 // A tile is 16 state rows, and two helpers finish it.  With at most one tile per SM a CTA takes one
 // tile, else two, which share the token tiles in shared memory.  2048 tokens, d = 128, forward by one / by two: 144 tiles
-// 101 / 110 us, 192 tiles 190 / 111; backward: 80 tiles 299 / 303, 256 tiles 669 / 572.
+// 106 / 122 us, 192 tiles 197 / 123; backward: 72 tiles 248 / 271, 144 tiles 382 / 359, 256 tiles 690 / 556.
 static bool few_tiles(const Call& c) { return (long long)c.d.B * c.d.h * (c.d.dv / 16) <= c.sms; }
 
 struct ChainOut {
@@ -381,14 +370,14 @@ struct Ctl {
 constexpr int kCtlBytes = 64;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
-template <int DK, int P, int PK, int RT, int KS, bool SAVE>
+template <int DK, int PK, int RT, int KS, bool SAVE>
 struct ChainLayout {
     static constexpr int VW = RT * 16;
     static constexpr int VB = VW * (PK == 1 ? 2 : 4);          // bytes of a row of the value tile
     static constexpr int kK = PK * CT * DK * 2;                // K of the period's chunk, then Q of the one before
     static constexpr int kQ = SAVE ? 0 : kK;
     static constexpr int kV = CT * VB;
-    static constexpr int kT = mat_bytes(PF), kA = SAVE ? 0 : mat_bytes(P);     // T', then A of the chunk before
+    static constexpr int kT = kMat, kA = SAVE ? 0 : kMat;     // T', then A of the chunk before
     static constexpr int stage = (kK + kQ + kV + kT + kA + 1023) / 1024 * 1024;
     static constexpr int kGates = kGateSlots * kGateBytes;
     static constexpr int kS = DK / 16 * P * 512;               // a tile's state as operand parts
@@ -401,23 +390,22 @@ struct ChainLayout {
     static_assert(VB <= 128 && kK % 1024 == 0 && kV % 1024 == 0, "swizzled tiles");
 };
 
-// acc (16 x 8) += (parts a of 16 rows x 32 k) * B for one block nb of 8 columns, B a lower-triangular matrix image
-// [PM parts][32][MP]; the products of the smallest parts first.  NT: B[k][n] = M[n][k] (columns n of the product are M's
+// acc (16 x 8) += (PA parts a of 16 rows x 32 k) * B for one block nb of 8 columns, B a lower-triangular matrix image
+// [P][32][MP]; the products of the smallest parts first.  NT: B[k][n] = M[n][k] (columns n of the product are M's
 // rows);  else B[k][n] = M[k][n].
-template <int PM, int PA, bool NT>
+template <int PA, bool NT>
 __device__ __forceinline__ void mat_block(float (&acc)[4], const uint32_t (&a)[2][PA][4], uint32_t mat, int nb, int lane) {
-    constexpr int P = PM > PA ? PM : PA;
     const int mi = lane >> 3, lr = lane & 7;
-    uint32_t b[PM][4];
+    uint32_t b[P][4];
 #pragma unroll
-    for (int pb = 0; pb < PM; ++pb) {
+    for (int pb = 0; pb < P; ++pb) {
         if (NT) ldsm4(b[pb], mat + ((pb * CT + nb * 8 + lr) * MP + mi * 8) * 2);
         else ldsm4t(b[pb], mat + ((pb * CT + mi * 8 + lr) * MP + nb * 8) * 2);
     }
 #pragma unroll
     for (int order = P - 1; order >= 0; --order)
 #pragma unroll
-        for (int pb = 0; pb < PM; ++pb) {
+        for (int pb = 0; pb < P; ++pb) {
             const int pa = order - pb;
             if (pa < 0 || pa >= PA) continue;
             if (NT || nb < 2) mma16816(acc, a[0][pa], b[pb][0], b[pb][1]);
@@ -426,26 +414,26 @@ __device__ __forceinline__ void mat_block(float (&acc)[4], const uint32_t (&a)[2
 }
 
 // The parts of accumulator blocks (2 kk, 2 kk + 1) as a left operand for k block kk.
-template <int P>
 __device__ __forceinline__ void as_operand(uint32_t (&a)[P][4], const float (&x)[4], const float (&y)[4]) {
     uint32_t o[P];
-    split2<P>(x[0], x[1], o);
+    split2(x[0], x[1], o);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][0] = o[p];
-    split2<P>(x[2], x[3], o);
+    split2(x[2], x[3], o);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][1] = o[p];
-    split2<P>(y[0], y[1], o);
+    split2(y[0], y[1], o);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][2] = o[p];
-    split2<P>(y[2], y[3], o);
+    split2(y[2], y[3], o);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][3] = o[p];
 }
 
 // A NaN or an infinity of one token must not reach the tokens before it, although a chunk's products meet it with zeros (0 x NaN is
 // NaN): where an operand's first parts show one (an infinity also stands for what bf16 cannot hold), such values count as zero, and results
-// from the first of a row on are NaN.  The look costs 469 against 440 us (forward, 32 heads of 8192 tokens, d = 128), nothing at d = 64.
+// from the first of a row on are NaN.  The look costs 488 against 470 us (forward, 32 heads of 8192 tokens, d = 128), nothing at d = 64.  (The
+// readout takes its product first and again where it has to: looking first, 525 us.)
 __device__ __forceinline__ bool not_finite(const uint32_t (&a)[4], const uint32_t (&b)[4]) {
     const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
     __nv_bfloat162 z[2] = {zero, zero};                    // 0 x: NaN of what is not finite
@@ -487,7 +475,7 @@ constexpr int kTilePart = CT * DK * 2;
 
 // s (16 x DW columns from col0) = fade s + (parts a: 16 x 32 tokens) * X, X a token tile.  Each block's products are
 // summed in accumulators of their own, the small ones first, and added to s in fp32.
-template <int DK, int DW, int P, int PK>
+template <int DK, int DW, int PK>
 __device__ __forceinline__ void fade_add_outer(float (&s)[DW / 8][4], float fade, const uint32_t (&a)[2][P][4], uint32_t x, int col0, int lane) {
     const int mi = lane >> 3, lr = lane & 7;
     const int c16 = col0 / 16;                     // first 16-column block: DW / 16 blocks, aligned to their number
@@ -521,7 +509,7 @@ __device__ __forceinline__ void fade_add_outer(float (&s)[DW / 8][4], float fade
 
 // acc (16 x 16 tokens, from token 16 n2) += (parts a: 16 x 16 features from col) * X^T, X a token tile: the products of the
 // first parts to acc, the others to low.
-template <int DK, int P, int PK>
+template <int DK, int PK>
 __device__ __forceinline__ void dot_tokens(float (&acc0)[4], float (&acc1)[4], float (&low0)[4], float (&low1)[4], const uint32_t (&a)[P][4],
                                            uint32_t x, int n2, int c16, int lane) {
     const int mi = lane >> 3, lr = lane & 7;
@@ -588,11 +576,10 @@ __device__ __forceinline__ void put_pair(uint32_t stage, const uint32_t (&w)[4],
     __syncwarp();
 }
 // As bf16 parts (x, y: the two blocks' accumulators), each part `ps` elements apart.
-template <int P>
 __device__ __forceinline__ void put_pair_parts(uint32_t stage, const float (&x)[4], const float (&y)[4], __nv_bfloat16* dst,
                                                long long ps, long long ts, int left, int lane) {
     uint32_t a[P][4];
-    as_operand<P>(a, x, y);
+    as_operand(a, x, y);
 #pragma unroll
     for (int p = 0; p < P; ++p) put_pair(stage + p * 16 * 48, a[p], dst + p * ps, ts, left, lane);
 }
@@ -618,7 +605,7 @@ __device__ __forceinline__ void put_pair_tokens(uint32_t stage, const float (&x)
 
 // A tile's operand parts in shared memory ([k block][part][lane] of 16 bytes) -> its rows [row0, row0 + 16) of the
 // state in global memory, bf16 parts [P][dv][DK]; helper `z` of kHelp takes every kHelp-th k block.
-template <int DK, int P>
+template <int DK>
 __device__ __forceinline__ void put_state_parts(uint32_t buf, __nv_bfloat16* dst, int dv, int row0, int z, int lane) {
     const int g = lane >> 2, t = lane & 3;
     for (int kk = z; kk < DK / 16; kk += kHelp)
@@ -733,10 +720,10 @@ __device__ __forceinline__ float lds1(uint32_t a) {
 // and leave the state they started from (as operand parts) and the residuals E in shared memory; the helpers finish
 // chunk c - 1 from those: its readout (forward), or E and the state to global memory (backward, SAVE);
 // the loading warp is one or two periods ahead.
-template <int DK, int P, int PK, int RT, int KS, bool SAVE>
+template <int DK, int PK, int RT, int KS, bool SAVE>
 __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const Tiled& K, const Tiled& V, const uint8_t* rec, const float* W0,
                                            long long w0_bs, const ChainOut& out, uint32_t* err, unsigned long long wait_ns, int block) {
-    using L = ChainLayout<DK, P, PK, RT, KS, SAVE>;
+    using L = ChainLayout<DK, PK, RT, KS, SAVE>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
     constexpr int DW = DK / KS, KB = DW / 16, NBW = 4 / KS, CW = RT * KS, HW = RT * kHelp;
@@ -756,7 +743,7 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
 
     if (warp == CW + HW) {
         // ---------------------------------------------------------------- loads
-        const int recb = rec_bytes(P, SAVE);
+        const int recb = rec_bytes(SAVE);
         const Abort ab{&ctl.abort_flag, err, wait_ns};
         if (lane == 0) {
             ctl.abort_flag = 0;
@@ -788,7 +775,7 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             }
             if (before) {
                 load_tokens<DK, PK>(l, st + L::kK, Q, b, h / d.r, c * CT - CT, left + CT);
-                l.flat(st + L::kK + L::kQ + L::kV + L::kT, r - recb + kRecA, L::kA);
+                l.flat(st + L::kK + L::kQ + L::kV + L::kT, r - recb + kGateBytes + kMat, L::kA);
             }
         };
         for (int c = 0; c < L::kStages - 1; ++c) issue(c);
@@ -814,10 +801,10 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             if constexpr (SAVE) {
                 const float4 v = lds4(ep + (2 * z * 32 + lane) * 16), w = lds4(ep + ((2 * z + 1) * 32 + lane) * 16);
                 const float e0[4] = {v.x, v.y, v.z, v.w}, e1[4] = {w.x, w.y, w.z, w.w};
-                put_pair_parts<P>(stagebuf, e0, e1, out.E + ((long long)bh * d.N + (long long)pc * CT + z * 16) * d.dv + row0, out.e_ps,
+                put_pair_parts(stagebuf, e0, e1, out.E + ((long long)bh * d.N + (long long)pc * CT + z * 16) * d.dv + row0, out.e_ps,
                                   d.dv, left - z * 16, lane);
                 if ((pc * CT) % d.gt == 0)
-                    put_state_parts<DK, P>(sp, out.S + ((long long)bh * d.ng + (pc * CT) / d.gt) * P * state, d.dv, row0, z, lane);
+                    put_state_parts<DK>(sp, out.S + ((long long)bh * d.ng + (pc * CT) / d.gt) * P * state, d.dv, row0, z, lane);
             } else {
                 // Z of tokens [16 z, 16 z + 16) = scale gamma (Q W^T) + A U
                 const uint32_t st = stage_of(c), qt = st + L::kK, am = st + L::kK + L::kQ + L::kV + L::kT;
@@ -830,7 +817,7 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                         const uint4 v = lds4u(sp + ((kk * P + p) * 32 + lane) * 16);
                         a[p][0] = v.x; a[p][1] = v.y; a[p][2] = v.z; a[p][3] = v.w;
                     }
-                    dot_tokens<DK, P, PK>(acc[0], acc[1], low[0], low[1], a, qt, z, kk, lane);
+                    dot_tokens<DK, PK>(acc[0], acc[1], low[0], low[1], a, qt, z, kk, lane);
                 }
                 float e[4][4];
 #pragma unroll
@@ -840,20 +827,22 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
                     e[nb][0] = be.x * v.x; e[nb][1] = be.y * v.y; e[nb][2] = be.x * v.z; e[nb][3] = be.y * v.w;
                 }
                 uint32_t u[2][P][4];
-                as_operand<P>(u[0], e[0], e[1]);
-                as_operand<P>(u[1], e[2], e[3]);
-                int first[2];
-                const bool hidden = not_finite(u[0][0], u[1][0]);
-                if (hidden) {
-                    hide_not_finite(e, first, lane);
-                    as_operand<P>(u[0], e[0], e[1]);
-                    as_operand<P>(u[1], e[2], e[3]);
-                }
+                as_operand(u[0], e[0], e[1]);
+                as_operand(u[1], e[2], e[3]);
                 float au[2][4] = {};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mat_block<P, P, true>(au[i], u, am, 2 * z + i, lane);
-                    if (hidden) mark_hidden(au[i], first, 2 * z + i, lane);
+                for (int i = 0; i < 2; ++i) mat_block<P, true>(au[i], u, am, 2 * z + i, lane);
+                if (not_finite(u[0][0], u[1][0])) {
+                    int first[2];
+                    hide_not_finite(e, first, lane);
+                    as_operand(u[0], e[0], e[1]);
+                    as_operand(u[1], e[2], e[3]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        au[i][0] = au[i][1] = au[i][2] = au[i][3] = 0.f;
+                        mat_block<P, true>(au[i], u, am, 2 * z + i, lane);
+                        mark_hidden(au[i], first, 2 * z + i, lane);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -883,11 +872,11 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
         float x[4][4] = {}, low[4][4] = {};
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
-            uint32_t a[PF][4];
-            as_operand<PF>(a, s[2 * kk], s[2 * kk + 1]);
+            uint32_t a[P][4];
+            as_operand(a, s[2 * kk], s[2 * kk + 1]);
 #pragma unroll
             for (int n2 = 0; n2 < 2; ++n2)
-                dot_tokens<DK, PF, PK>(x[2 * n2], x[2 * n2 + 1], low[2 * n2], low[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
+                dot_tokens<DK, PK>(x[2 * n2], x[2 * n2 + 1], low[2 * n2], low[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
             if (hand) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) sts4u(sp + (((ks * KB + kk) * P + p) * 32 + lane) * 16, a[p]);
@@ -934,18 +923,18 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
         }
         // E = T' R
         float e[4][4] = {};
-        uint32_t a[2][PF][4];
-        as_operand<PF>(a[0], x[0], x[1]);
-        as_operand<PF>(a[1], x[2], x[3]);
+        uint32_t a[2][P][4];
+        as_operand(a[0], x[0], x[1]);
+        as_operand(a[1], x[2], x[3]);
         int first[2];
         const bool hidden = not_finite(a[0][0], a[1][0]);
         if (hidden) {
             hide_not_finite(x, first, lane);
-            as_operand<PF>(a[0], x[0], x[1]);
-            as_operand<PF>(a[1], x[2], x[3]);
+            as_operand(a[0], x[0], x[1]);
+            as_operand(a[1], x[2], x[3]);
         }
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) mat_block<PF, PF, true>(e[nb], a, tm, nb, lane);
+        for (int nb = 0; nb < 4; ++nb) mat_block<P, true>(e[nb], a, tm, nb, lane);
         if (hidden)
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) mark_hidden(e[nb], first, nb, lane);
@@ -957,9 +946,9 @@ __device__ __forceinline__ void chain_body(const Dims& d, const Tiled& Q, const 
             const float u0 = su.x * be.x, u1 = su.y * be.y;
             e[nb][0] *= u0; e[nb][1] *= u1; e[nb][2] *= u0; e[nb][3] *= u1;
         }
-        as_operand<PF>(a[0], e[0], e[1]);
-        as_operand<PF>(a[1], e[2], e[3]);
-        fade_add_outer<DK, DW, PF, PK>(s, lds1(gt + (CT - 1) * 4), a, kt, col0, lane);
+        as_operand(a[0], e[0], e[1]);
+        as_operand(a[1], e[2], e[3]);
+        fade_add_outer<DK, DW, PK>(s, lds1(gt + (CT - 1) * 4), a, kt, col0, lane);
     }
     if (out.W1) put_state<DK, DW>(s, out.W1 + (long long)bh * state, row0, col0, lane);
 }
@@ -974,11 +963,11 @@ struct ChainArgs {
     uint32_t* err;
     unsigned long long wait_ns;
 };
-template <int DK, int P, int PK, int RT, int KS>
+template <int DK, int PK, int RT, int KS>
 __global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
 delta_chain(const __grid_constant__ ChainArgs a) {
     pdl_launch_dependents();
-    chain_body<DK, P, PK, RT, KS, false>(a.d, a.Q, a.K, a.V, a.rec, a.W0, a.w0_bs, a.out, a.err, a.wait_ns, blockIdx.x);
+    chain_body<DK, PK, RT, KS, false>(a.d, a.Q, a.K, a.V, a.rec, a.W0, a.w0_bs, a.out, a.err, a.wait_ns, blockIdx.x);
 }
 
 // A five-dimensional tensor map: boxes of `rows` along the second dimension x rb bytes (32, 64 or 128, swizzled alike)
@@ -1027,8 +1016,8 @@ static Tiled tiled(const Parts& x, int parts, const Dims& d, int heads, int widt
 
 // Launches `k` as a programmatic dependent of what precedes it in the stream: its set-up overlaps that kernel's tail.
 // (Every kernel here waits for its predecessor before it reads or writes global memory.  split_tokens and the step are plain launches.)
-template <class... P, class... A>
-static ttt_status launch(void (*k)(P...), long long grid, int threads, int smem, cudaStream_t st, A... args) {
+template <class... T, class... A>
+static ttt_status launch(void (*k)(T...), long long grid, int threads, int smem, cudaStream_t st, A... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1039,7 +1028,7 @@ static ttt_status launch(void (*k)(P...), long long grid, int threads, int smem,
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return check_launch(cudaLaunchKernelEx(&cfg, k, P(args)...));
+    return check_launch(cudaLaunchKernelEx(&cfg, k, T(args)...));
 }
 
 // Shared memory that leaves room for no second CTA of the same kernel on an SM: a grid that fits the SMs is spread over
@@ -1071,12 +1060,11 @@ struct Layout {
     size_t rec, qp, kp, op, E, Y, S, D, dw, part, total;
 };
 static Layout layout(const Dims& d, bool fp32, bool backward) {
-    const int P = fp32 || backward ? PF : 2;
     Layout l{};
     size_t at = kWsHeader;
     auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
     const size_t heads = (size_t)d.B * d.h, toks = heads * d.N;
-    l.rec = take(heads * d.nc * rec_bytes(P, backward));
+    l.rec = take(heads * d.nc * rec_bytes(backward));
     if (fp32) {
         l.qp = take((size_t)3 * d.B * d.hk * d.N * d.dk * 2);
         l.kp = take((size_t)3 * d.B * d.hk * d.N * d.dk * 2);
@@ -1121,26 +1109,26 @@ struct Splitter {
         a.d = c.d;
         long long most = 0;
         for (int i = 0; i < n; ++i) most = std::max(most, a.ps[i]);
-        split_tokens<3><<<dim3((unsigned)std::min<long long>((most / 4 + 255) / 256, 8LL * c.sms), n), 256, 0, c.stream>>>(a);
+        split_tokens<<<dim3((unsigned)std::min<long long>((most / 4 + 255) / 256, 8LL * c.sms), n), 256, 0, c.stream>>>(a);
         return check_launch(cudaGetLastError());
     }
 };
 
-template <int DK, int P, int PK, bool BACKWARD>
+template <int DK, int PK, bool BACKWARD>
 static ttt_status run_prep(const Call& c, const Parts& Q, const Parts& K, uint8_t* rec) {
     constexpr int smem = kPrepWarps * kPrepWarpBytes;
-    constexpr auto k = delta_prep<DK, P, PK, BACKWARD>;
+    constexpr auto k = delta_prep<DK, PK, BACKWARD>;
     ttt_status st = allow_smem<k>(smem);
     if (st != TTT_OK) return st;
     const long long total = (long long)c.d.B * c.d.h * c.d.nc;
     return launch(k, (total + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, smem, c.stream, c.d, Q, K, c.G, c.Beta, rec, total, error_word(c));
 }
 
-template <int DK, int P, int PK, int RT, int KS>
+template <int DK, int PK, int RT, int KS>
 static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, const uint8_t* rec, const ChainOut& out) {
-    using L = ChainLayout<DK, P, PK, RT, KS, false>;
+    using L = ChainLayout<DK, PK, RT, KS, false>;
     static_assert(L::smem <= 227 * 1024, "shared memory of a chain CTA");
-    constexpr auto k = delta_chain<DK, P, PK, RT, KS>;
+    constexpr auto k = delta_chain<DK, PK, RT, KS>;
     const ttt_status st = allow_smem<k>(std::max(L::smem, kAloneSmem));
     if (st != TTT_OK) return st;
     const long long grid = (long long)c.d.B * c.d.h * (c.d.dv / L::VW);
@@ -1150,21 +1138,21 @@ static ttt_status run_chain_t(const Call& c, const Parts& Q, const Parts& K, con
     return launch(k, grid, seq_warps<RT, KS>() * 32, spread_smem(L::smem, grid, c.sms), c.stream, a);
 }
 
-template <int DK, int P, int PK>
+template <int DK, int PK>
 static ttt_status forward_t(const Call& c) {
     const Layout l = layout(c.d, PK == 3, false);
     Splitter split{c, PK == 3};
     const Parts Q = split.add(c.Q, c.ws + l.qp, c.d.hk, DK), K = split.add(c.K, c.ws + l.kp, c.d.hk, DK);
     ttt_status st = split.run();
-    if (st == TTT_OK) st = run_prep<DK, P, PK, false>(c, Q, K, c.ws + l.rec);
+    if (st == TTT_OK) st = run_prep<DK, PK, false>(c, Q, K, c.ws + l.rec);
     if (st != TTT_OK) return st;
     ChainOut out{};
     out.Z = c.Z;
     out.W1 = c.W1_out;
-    return few_tiles(c) ? run_chain_t<DK, P, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, P, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
+    return few_tiles(c) ? run_chain_t<DK, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
 }
 
-template <int DK, int P, int PK>
+template <int DK, int PK>
 static ttt_status backward_t(const Call& c) {
     constexpr bool F = PK == 3;
     const Layout l = layout(c.d, F, true);
@@ -1186,20 +1174,20 @@ static ttt_status backward_t(const Call& c) {
                 O = split.add(c.Z, c.ws + l.op, c.d.h, c.d.dv);
     ttt_status st = split.run();
     if (st != TTT_OK) return st;
-    st = run_prep<DK, P, PK, true>(c, Q, K, rec);
-    if (st == TTT_OK) st = run_both<DK, P, PK>(c, Q, K, O, rec, out, bo);
+    st = run_prep<DK, PK, true>(c, Q, K, rec);
+    if (st == TTT_OK) st = run_both<DK, PK>(c, Q, K, O, rec, out, bo);
     if (st == TTT_OK) st = run_grads<DK, PK>(c, Q, K, O, out, bo, reinterpret_cast<float*>(c.ws + l.part));
     if (st != TTT_OK || !reduce) return st;
     return run_sum_images(bo.dW0, c.dW0, c.d.B, (long long)c.d.h * c.d.dv * DK, c.stream);
 }
 
 ttt_status launch_forward(const Call& c) {
-    if (c.fp32) return c.d.dk == 64 ? forward_t<64, PF, 3>(c) : forward_t<128, PF, 3>(c);
-    return c.d.dk == 64 ? forward_t<64, 2, 1>(c) : forward_t<128, 2, 1>(c);
+    if (c.fp32) return c.d.dk == 64 ? forward_t<64, 3>(c) : forward_t<128, 3>(c);
+    return c.d.dk == 64 ? forward_t<64, 1>(c) : forward_t<128, 1>(c);
 }
 ttt_status launch_backward(const Call& c) {
-    if (c.fp32) return c.d.dk == 64 ? backward_t<64, PF, 3>(c) : backward_t<128, PF, 3>(c);
-    return c.d.dk == 64 ? backward_t<64, PF, 1>(c) : backward_t<128, PF, 1>(c);
+    if (c.fp32) return c.d.dk == 64 ? backward_t<64, 3>(c) : backward_t<128, 3>(c);
+    return c.d.dk == 64 ? backward_t<64, 1>(c) : backward_t<128, 1>(c);
 }
 
 }  // namespace gd

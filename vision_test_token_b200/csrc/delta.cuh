@@ -35,15 +35,13 @@ struct Dims {
     float scale;
 };
 
-// bf16 parts of an operand that an fp32 result comes from: 24 bits, as many as fp32 has.
-constexpr int PF = 3;
+// bf16 parts of an operand that no bf16 value holds: 24 bits, as many as fp32 has.
+constexpr int P = 3;
 // Per (image, value head, chunk) record in the workspace, written by the prep kernel and copied as it
-// is into shared memory: gates (gamma, suffix, beta), then the bf16 part images of T' (PF parts), A (P parts) and (backward)
-// T_u (PF parts).
+// is into shared memory: gates (gamma, suffix, beta), then the part images of T', A and (backward) T_u.
 constexpr int kGateBytes = 3 * CT * 4;
-__host__ __device__ constexpr int mat_bytes(int P) { return P * CT * MP * 2; }
-constexpr int kRecA = kGateBytes + mat_bytes(PF);            // offset of A
-__host__ __device__ constexpr int rec_bytes(int P, bool backward) { return kRecA + mat_bytes(P) + (backward ? mat_bytes(PF) : 0); }
+constexpr int kMat = P * CT * MP * 2;
+__host__ __device__ constexpr int rec_bytes(bool backward) { return kGateBytes + (backward ? 3 : 2) * kMat; }
 
 struct Call {
     Dims d;
@@ -118,10 +116,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// (x, y) as P packed bf16 pairs whose sum is (x, y) up to 2^-8P relative: part 0 is the nearest bf16,
+// (x, y) as P packed bf16 pairs whose sum is (x, y) up to 2^-24 relative: part 0 is the nearest bf16,
 // part p the nearest bf16 to what the earlier parts leave.  (An infinite value gives NaN parts: a state
 // that overflowed ends in NaN.)
-template <int P>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&o)[P]) {
     o[0] = pack2(x, y);
 #pragma unroll

@@ -16,9 +16,9 @@
 //   write and readout, which a strong gate does not touch, would leave only their rounding.)
 //   E and W come from the forward chain run again (they are not kept from the forward call).
 // The two sequential sweeps need nothing of each other and run side by side in one launch (24 ragged heads of up to
-// 1531 tokens, d = 128: 138 us).
-// Every inexact operand is three bf16 parts (for bf16 tokens two in H K, F K, H^T Q and F^T K, which end in dQ and dK alone, rounded to
-// eight bits).  Two parts throughout were off by 3e-6 (dW0) to 6e-6 (dbeta) in the 2-norm, a plain fp32 computation by 1 to 3e-7.
+// 1531 tokens, d = 128: 127 us).
+// Every inexact operand is three bf16 parts, as in the forward pass.  (Two parts throughout were off by 3e-6 (dW0) to 6e-6 (dbeta) in the
+// 2-norm, a plain fp32 computation by 1 to 3e-7.)
 
 struct BackOut {
     View dV;
@@ -28,14 +28,12 @@ struct BackOut {
     float* dW0;                   // nullable [B][h][dv][dk]
 };
 
-template <int DK, int P, int PK, int RT, int KS>
+template <int DK, int PK, int RT, int KS>
 struct ReverseLayout {
     static constexpr int VW = RT * 16, VB = VW * 2;
     static constexpr int kK = PK * CT * DK * 2;                // K, Q and T_u of the period's chunk,
     static constexpr int kO1 = CT * VB, kO = PK * kO1;         // dZ and A of the next one
-    static constexpr int kM = mat_bytes(P);
-    static_assert(P == PF, "A and T_u have the same parts");
-    static constexpr int stage = (2 * kK + kO + 2 * kM + 1023) / 1024 * 1024;
+    static constexpr int stage = (2 * kK + kO + 2 * kMat + 1023) / 1024 * 1024;
     static constexpr int kGates = kGateSlots * kGateBytes;
     static constexpr int kS = DK / 16 * P * 512;               // a tile's adjoint as operand parts
     static constexpr int kE = 2048;                            // Y, A^T dZ, partial sums
@@ -51,10 +49,10 @@ struct ReverseLayout {
 // Periods k = -1 .. chunks, chunks counted from the last.  In period k the chain warps take chunk k; the helpers
 // prepare what chunk k + 1 needs of dZ alone (A^T dZ, and scale gamma dZ as operand parts) and write what chunk
 // k - 1 gave (Y, dV, and the adjoint it started from).
-template <int DK, int P, int PK, int RT, int KS>
+template <int DK, int PK, int RT, int KS>
 __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, const Tiled& K, const Tiled& O, const uint8_t* rec, const float* dW1,
                                              const BackOut& out, uint32_t* err, unsigned long long wait_ns, int block) {
-    using L = ReverseLayout<DK, P, PK, RT, KS>;
+    using L = ReverseLayout<DK, PK, RT, KS>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (s32(smem_raw) & 1023));
     constexpr int DW = DK / KS, KB = DW / 16, NBW = 4 / KS, CW = RT * KS, HW = RT * kHelp;
@@ -75,7 +73,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
 
     if (warp == CW + HW) {
         // ---------------------------------------------------------------- loads
-        const int recb = rec_bytes(P, true);
+        const int recb = rec_bytes(true);
         const Abort ab{&ctl.abort_flag, err, wait_ns};
         if (lane == 0) {
             ctl.abort_flag = 0;
@@ -93,15 +91,15 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             if (lane == 0) {
                 fence_proxy_async_smem();             // the warp's own stores to the stage, before the copies' writes
                 uint32_t n = 0;
-                if (now) n += Loader::bytes(K, len - c * CT, L::kK) + Loader::bytes(Q, len - c * CT, L::kK) + L::kM;
-                if (next) n += Loader::bytes(O, len - (c - 1) * CT, L::kO) + kGateBytes + L::kM;
+                if (now) n += Loader::bytes(K, len - c * CT, L::kK) + Loader::bytes(Q, len - c * CT, L::kK) + kMat;
+                if (next) n += Loader::bytes(O, len - (c - 1) * CT, L::kO) + kGateBytes + kMat;
                 mbar_arrive_expect_tx(l.bar, n);
             }
             __syncwarp();
             if (now) {
                 load_tokens<DK, PK>(l, st, K, b, h / d.r, c * CT, len - c * CT);
                 load_tokens<DK, PK>(l, st + L::kK, Q, b, h / d.r, c * CT, len - c * CT);
-                l.flat(st + 2 * L::kK + L::kO, rec + ((long long)bh * d.nc + c) * recb + kRecA + L::kM, L::kM);
+                l.flat(st + 2 * L::kK + L::kO, rec + ((long long)bh * d.nc + c) * recb + kGateBytes + 2 * kMat, kMat);
             }
             if (next) {
                 const uint8_t* r = rec + ((long long)bh * d.nc + c - 1) * recb;
@@ -109,7 +107,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
                 for (int p = 0; p < PK; ++p)
                     l.template tile<L::VB, 2>(st + 2 * L::kK + p * L::kO1, O, p, b, h, (c - 1) * CT, v0, len - (c - 1) * CT);
                 l.flat(gate_slot(k + 1), r, kGateBytes);
-                l.flat(st + 2 * L::kK + L::kO + L::kM, r + kRecA, L::kM);
+                l.flat(st + 2 * L::kK + L::kO + kMat, r + kGateBytes + kMat, kMat);
             }
         };
         for (int k = -1; k < L::kStages - 2; ++k) issue(k);
@@ -132,7 +130,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             __syncthreads();
             if (k + 1 < nch) {
                 const int n = k + 1, mi = lane >> 3, lr = lane & 7;
-                const uint32_t st = stage_of(k), ot = st + 2 * L::kK, am = ot + L::kO + L::kM, gt = gate_slot(n);
+                const uint32_t st = stage_of(k), ot = st + 2 * L::kK, am = ot + L::kO + kMat, gt = gate_slot(n);
                 uint32_t o[2][PK][4];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
@@ -142,7 +140,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float acc[4] = {};
-                    mat_block<P, PK, false>(acc, o, am, 2 * z + i, lane);
+                    mat_block<PK, false>(acc, o, am, 2 * z + i, lane);
                     sts4(abuf + ((n & 1) * RT + rt) * L::kE + ((2 * z + i) * 32 + lane) * 16, acc);
                 }
                 // tokens 16 z + 2t (+1), then + 8; none behind the end of the sequence
@@ -162,7 +160,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
                     f[q >> 1][2 * (q & 1) + 1] = 8 * (q >> 1) + 1 < tl ? hi * (d.scale * ((q >> 1) ? g1.y : g0.y)) : 0.f;
                 }
                 uint32_t a[P][4];
-                as_operand<P>(a, f[0], f[1]);
+                as_operand(a, f[0], f[1]);
 #pragma unroll
                 for (int p = 0; p < P; ++p) sts4u(fbuf + ((n & 1) * RT + rt) * L::kF + ((z * P + p) * 32 + lane) * 16, a[p]);
             }
@@ -171,7 +169,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
                 const uint32_t yp = ybuf + ((n & 1) * RT + rt) * L::kE, gt = gate_slot(n);
                 const float4 v = lds4(yp + (2 * z * 32 + lane) * 16), w = lds4(yp + ((2 * z + 1) * 32 + lane) * 16);
                 const float y0[4] = {v.x, v.y, v.z, v.w}, y1[4] = {w.x, w.y, w.z, w.w};
-                put_pair_parts<P>(stagebuf, y0, y1, out.Y + ((long long)bh * d.N + (long long)c * CT + z * 16) * d.dv + row0, out.y_ps,
+                put_pair_parts(stagebuf, y0, y1, out.Y + ((long long)bh * d.N + (long long)c * CT + z * 16) * d.dv + row0, out.y_ps,
                                   d.dv, left - z * 16, lane);
                 const float2 b0 = lds2(gt + (2 * CT + z * 16 + 2 * t) * 4), b1 = lds2(gt + (2 * CT + z * 16 + 8 + 2 * t) * 4);
                 const float d0[4] = {b0.x * v.x, b0.y * v.y, b0.x * v.z, b0.y * v.w};
@@ -180,7 +178,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
                                     b * out.dV.bs + h * out.dV.hs + ((long long)c * CT + z * 16) * out.dV.ts + row0, out.dV.ts, left - z * 16,
                                     lane);
                 if (n == 0 || ((c + 1) * CT) % d.gt == 0)
-                    put_state_parts<DK, P>(sbuf + ((n & 1) * RT + rt) * L::kS,
+                    put_state_parts<DK>(sbuf + ((n & 1) * RT + rt) * L::kS,
                                            out.D + ((long long)bh * d.ng + (c * CT) / d.gt) * P * state, d.dv, row0, z, lane);
             }
         }
@@ -205,10 +203,10 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
             uint32_t a[P][4];
-            as_operand<P>(a, s[2 * kk], s[2 * kk + 1]);
+            as_operand(a, s[2 * kk], s[2 * kk + 1]);
 #pragma unroll
             for (int n2 = 0; n2 < 2; ++n2)
-                dot_tokens<DK, P, PK>(x[2 * n2], x[2 * n2 + 1], low[2 * n2], low[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
+                dot_tokens<DK, PK>(x[2 * n2], x[2 * n2 + 1], low[2 * n2], low[2 * n2 + 1], a, kt, n2, ks * KB + kk, lane);
             if (hand) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) sts4u(sp + (((ks * KB + kk) * P + p) * 32 + lane) * 16, a[p]);
@@ -231,7 +229,7 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
                 const uint4 v = lds4u(fp + ((kk * P + p) * 32 + lane) * 16);
                 a[kk][p][0] = v.x; a[kk][p][1] = v.y; a[kk][p][2] = v.z; a[kk][p][3] = v.w;
             }
-        fade_add_outer<DK, DW, P, PK>(s, lds1(gt + (CT - 1) * 4), a, qt, col0, lane);
+        fade_add_outer<DK, DW, PK>(s, lds1(gt + (CT - 1) * 4), a, qt, col0, lane);
         if constexpr (KS > 1) {
             tile_sync<KS>(rt);
 #pragma unroll
@@ -248,10 +246,10 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
         }
         // Y = T_u^T dU
         float y[4][4] = {};
-        as_operand<P>(a[0], x[0], x[1]);
-        as_operand<P>(a[1], x[2], x[3]);
+        as_operand(a[0], x[0], x[1]);
+        as_operand(a[1], x[2], x[3]);
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) mat_block<P, P, false>(y[nb], a, um, nb, lane);
+        for (int nb = 0; nb < 4; ++nb) mat_block<P, false>(y[nb], a, um, nb, lane);
         // D -= (gamma beta Y)^T K
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
@@ -260,9 +258,9 @@ __device__ __forceinline__ void reverse_body(const Dims& d, const Tiled& Q, cons
             const float u0 = -ga.x * be.x, u1 = -ga.y * be.y;
             y[nb][0] *= u0; y[nb][1] *= u1; y[nb][2] *= u0; y[nb][3] *= u1;
         }
-        as_operand<P>(a[0], y[0], y[1]);
-        as_operand<P>(a[1], y[2], y[3]);
-        fade_add_outer<DK, DW, P, PK>(s, 1.f, a, kt, col0, lane);
+        as_operand(a[0], y[0], y[1]);
+        as_operand(a[1], y[2], y[3]);
+        fade_add_outer<DK, DW, PK>(s, 1.f, a, kt, col0, lane);
     }
     if (out.dW0) put_state<DK, DW>(s, out.dW0 + bh * state, row0, col0, lane);
 }
@@ -280,14 +278,14 @@ struct BothArgs {
     unsigned long long wait_ns;
     int half;                     // CTAs of each
 };
-template <int DK, int P, int PK, int RT, int KS>
+template <int DK, int PK, int RT, int KS>
 __global__ void __launch_bounds__(seq_warps<RT, KS>() * 32)
 delta_both(const __grid_constant__ BothArgs a) {
     pdl_launch_dependents();
     if ((int)blockIdx.x < a.half)
-        reverse_body<DK, P, PK, RT, KS>(a.d, a.Q, a.K, a.O, a.rec, a.dW1, a.back, a.err, a.wait_ns, blockIdx.x);
+        reverse_body<DK, PK, RT, KS>(a.d, a.Q, a.K, a.O, a.rec, a.dW1, a.back, a.err, a.wait_ns, blockIdx.x);
     else
-        chain_body<DK, P, PK, RT, KS, true>(a.d, a.Q, a.K, a.V, a.rec, a.W0, a.w0_bs, a.chain, a.err, a.wait_ns, blockIdx.x - a.half);
+        chain_body<DK, PK, RT, KS, true>(a.d, a.Q, a.K, a.V, a.rec, a.W0, a.w0_bs, a.chain, a.err, a.wait_ns, blockIdx.x - a.half);
 }
 
 // --------------------------------------------------------------------------------------------------
@@ -295,16 +293,15 @@ delta_both(const __grid_constant__ BothArgs a) {
 // --------------------------------------------------------------------------------------------------
 template <int DK, int PK>
 struct GradsLayout {
-    static constexpr int PX = PK == 1 ? 2 : PF;                 // parts of what ends in gradients of the tokens' type alone
     static constexpr int GT = PK == 3 ? 32 : 64;                // tokens per group
     static constexpr int SV = 32;                               // value features per slice
     static constexpr int KP = DK + 8, SP = SV + 8, HP = GT + 8, FP = GT + 1;
     static constexpr int kK = PK * GT * KP * 2;                 // K, and Q
     static constexpr int kO = PK * GT * SP * 2;
-    static constexpr int kE = PF * GT * SP * 2;                 // E, and Y
-    static constexpr int kS = PF * SV * KP * 2;                 // W, and D
+    static constexpr int kE = P * GT * SP * 2;                 // E, and Y
+    static constexpr int kS = P * SV * KP * 2;                 // W, and D
     static constexpr int stage = kO + 2 * kE + 2 * kS;
-    static constexpr int kH = PX * GT * HP * 2;                // H, and F: in the stages' memory after the slices
+    static constexpr int kH = P * GT * HP * 2;                // H, and F: in the stages' memory after the slices
     static constexpr int WM = GT / 16, WN = 8 / WM;             // warps along the tokens, and along the columns
     static constexpr int kRed = (2 * WN + WM) * GT + 8;         // partial row and column sums, then 8 warps' <D, W>
     static constexpr int kG = (GT * FP + 5 * GT) * 4;           // Gamma, gate rows and dbeta
@@ -313,48 +310,46 @@ struct GradsLayout {
     static_assert(smem <= 227 * 1024, "shared memory of a gradient CTA");
 };
 
-// (c0, c1) += a * (b[.][0], b[.][1]), (b[.][2], b[.][3]): the parts of 16 x 16 times 16 x 16, products of the parts below the P-th
-// dropped.  FRESH: summed in accumulators of their own, the small products first, and added in fp32.
-template <int P, bool FRESH, int NA, int NB>
+// (c0, c1) += a * (b[.][0], b[.][1]), (b[.][2], b[.][3]): 16 x 16 times 16 x 16 of NA and NB parts, products of parts below the MOST-th
+// dropped; summed in accumulators of their own, the small products first, and added in fp32.
+template <int MOST, int NA, int NB>
 __device__ __forceinline__ void add_product(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4]) {
     float u0[4] = {}, u1[4] = {};
 #pragma unroll
-    for (int order = P - 1; order >= 0; --order)
+    for (int order = MOST - 1; order >= 0; --order)
 #pragma unroll
         for (int pb = 0; pb < NB; ++pb) {
             const int pa = order - pb;
             if (pa < 0 || pa >= NA) continue;
-            mma16816(FRESH ? u0 : c0, a[pa], b[pb][0], b[pb][1]);
-            mma16816(FRESH ? u1 : c1, a[pa], b[pb][2], b[pb][3]);
+            mma16816(u0, a[pa], b[pb][0], b[pb][1]);
+            mma16816(u1, a[pa], b[pb][2], b[pb][3]);
         }
-    if (FRESH)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            c0[q] += u0[q];
-            c1[q] += u1[q];
-        }
+    for (int q = 0; q < 4; ++q) {
+        c0[q] += u0[q];
+        c1[q] += u1[q];
+    }
 }
 
 struct GradsArgs {
     Dims d;
     Parts Q, K, O;
     View G, Beta;
-    const __nv_bfloat16 *E, *Y;       // [PF][B][h][N][dv], parts eps apart
+    const __nv_bfloat16 *E, *Y;       // [P][B][h][N][dv], parts eps apart
     long long eps;
-    const __nv_bfloat16 *S, *D;       // states at the groups' starts, adjoints at their ends [B][h][ng][PF][dv][dk]
+    const __nv_bfloat16 *S, *D;       // states at the groups' starts, adjoints at their ends [B][h][ng][P][dv][dk]
     View dQ, dK, dG, dBeta;
     float* part;                      // nullable: fp32 dQ, then dK, per value head [2][B][h][N][dk] instead
 };
 
-// Bound: latency, one CTA of eight warps per SM (the matrix instructions of a group are about 160 us of the following).  32 heads of
-// 4096 tokens, d = 128: 450 us.
+// Bound: latency, one CTA of eight warps per SM (the tensor pipe is busy 38 % of the time).  32 heads of
+// 4096 tokens, d = 128: 470 us.
 template <int DK, int PK>
 __global__ void __launch_bounds__(256)
 delta_grads(const __grid_constant__ GradsArgs p) {
     using L = GradsLayout<DK, PK>;
-    constexpr int PX = L::PX, GT = L::GT, SV = L::SV, KP = L::KP, SP = L::SP, HP = L::HP, FP = L::FP, NT = 256;
+    constexpr int GT = L::GT, SV = L::SV, KP = L::KP, SP = L::SP, HP = L::HP, FP = L::FP, NT = 256;
     constexpr int WM = L::WM, WN = L::WN, NBA = GT / WN / 8, DKW = DK / WN, NBK = DKW / 8;
-    constexpr bool FX = PK == 3;                                // dK is fp32 too
     extern __shared__ __align__(16) uint8_t smem[];
     const Dims& d = p.d;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -396,7 +391,7 @@ delta_grads(const __grid_constant__ GradsArgs p) {
         rows(qt + q * GT * KP * 2, KP, p.Q.p + q * p.Q.ps + b * p.Q.bs + kh * p.Q.hs + tok * p.Q.ts, p.Q.ts, DK);
     }
     const int ns = d.dv / SV;
-    const long long state = (long long)d.dv * DK, so0 = (bh * d.ng + grp) * PF * state;
+    const long long state = (long long)d.dv * DK, so0 = (bh * d.ng + grp) * P * state;
     const int i0 = wm * 16 + g;                                 // this lane's rows: i0, i0 + 8
 
     auto issue = [&](int sl) {
@@ -406,7 +401,7 @@ delta_grads(const __grid_constant__ GradsArgs p) {
             for (int q = 0; q < PK; ++q)
                 rows(st + q * GT * SP * 2, SP, p.O.p + q * p.O.ps + b * p.O.bs + h * p.O.hs + tok * p.O.ts + sl * SV, p.O.ts, SV);
 #pragma unroll
-            for (int q = 0; q < PF; ++q) {
+            for (int q = 0; q < P; ++q) {
                 const long long eo = q * p.eps + (bh * d.N + tok) * d.dv + sl * SV;
                 rows(et + q * GT * SP * 2, SP, p.E + eo, d.dv, SV);
                 rows(yt + q * GT * SP * 2, SP, p.Y + eo, d.dv, SV);
@@ -471,41 +466,41 @@ delta_grads(const __grid_constant__ GradsArgs p) {
         const uint32_t arow = ((wm * 16 + (mi & 1) * 8 + lr) * SP + (mi >> 1) * 8) * 2;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            uint32_t ao[PK][4], ae[PF][4], ay[PF][4];
+            uint32_t ao[PK][4], ae[P][4], ay[P][4];
 #pragma unroll
             for (int q = 0; q < PK; ++q) ldsm4(ao[q], ot + q * GT * SP * 2 + arow + kk * 32);
 #pragma unroll
-            for (int q = 0; q < PF; ++q) {
+            for (int q = 0; q < P; ++q) {
                 ldsm4(ae[q], et + q * GT * SP * 2 + arow + kk * 32);
                 ldsm4(ay[q], yt + q * GT * SP * 2 + arow + kk * 32);
             }
 #pragma unroll
             for (int n2 = 0; n2 < NBK / 2; ++n2) {
                 const uint32_t bo = ((kk * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2;
-                uint32_t w[PF][4];
+                uint32_t w[P][4];
 #pragma unroll
-                for (int q = 0; q < PF; ++q) ldsm4t(w[q], wt + q * SV * KP * 2 + bo);
-                add_product<PF, true>(fq[2 * n2], fq[2 * n2 + 1], ao, w);
-                add_product<PF, true>(f5[2 * n2], f5[2 * n2 + 1], ay, w);
+                for (int q = 0; q < P; ++q) ldsm4t(w[q], wt + q * SV * KP * 2 + bo);
+                add_product<P>(fq[2 * n2], fq[2 * n2 + 1], ao, w);
+                add_product<P>(f5[2 * n2], f5[2 * n2 + 1], ay, w);
 #pragma unroll
-                for (int q = 0; q < PF; ++q) ldsm4t(w[q], dt + q * SV * KP * 2 + bo);
-                add_product<PF, true>(f4[2 * n2], f4[2 * n2 + 1], ae, w);
+                for (int q = 0; q < P; ++q) ldsm4t(w[q], dt + q * SV * KP * 2 + bo);
+                add_product<P>(f4[2 * n2], f4[2 * n2 + 1], ae, w);
             }
 #pragma unroll
             for (int nb = 0; nb < NBA; nb += NB2) {
                 if (wn * (GT / WN) + nb * 8 > wm * 16 + 15) continue;
-                uint32_t x[PF][4];
+                uint32_t x[P][4];
 #pragma unroll
-                for (int q = 0; q < PF; ++q) columns(x[q], et + q * GT * SP * 2, SP, nb, kk);
-                add_product<PF, true>(aq[nb], NB2 > 1 ? aq[nb + NB2 - 1] : none, ao, x);
-                add_product<PF, true>(al[nb], NB2 > 1 ? al[nb + NB2 - 1] : none, ay, x);
+                for (int q = 0; q < P; ++q) columns(x[q], et + q * GT * SP * 2, SP, nb, kk);
+                add_product<P>(aq[nb], NB2 > 1 ? aq[nb + NB2 - 1] : none, ao, x);
+                add_product<P>(al[nb], NB2 > 1 ? al[nb + NB2 - 1] : none, ay, x);
             }
         }
         for (int x = tid; x < SV * DK / 2; x += NT) {           // <D, W> of the slice
             const uint32_t o = (x / (DK / 2) * KP + x % (DK / 2) * 2) * 2;
             float w0 = 0.f, w1 = 0.f, d0 = 0.f, d1 = 0.f;
 #pragma unroll
-            for (int q = PF - 1; q >= 0; --q) {
+            for (int q = P - 1; q >= 0; --q) {
                 const uint32_t a = *reinterpret_cast<const uint32_t*>(smem + (wt - sb) + q * SV * KP * 2 + o);
                 const uint32_t z = *reinterpret_cast<const uint32_t*>(smem + (dt - sb) + q * SV * KP * 2 + o);
                 w0 += lo_f(a); w1 += hi_f(a); d0 += lo_f(z); d1 += hi_f(z);
@@ -532,10 +527,10 @@ delta_grads(const __grid_constant__ GradsArgs p) {
                     columns(x[q], kt + q * GT * KP * 2, KP, nb, kk);
                     ldsm4(a[q], qt + q * GT * KP * 2 + arow + kk * 32);
                 }
-                add_product<PK, PK == 3>(qk[0], qk[1], a, x);
+                add_product<PK>(qk[0], qk[1], a, x);
 #pragma unroll
                 for (int q = 0; q < PK; ++q) ldsm4(a[q], kt + q * GT * KP * 2 + arow + kk * 32);
-                add_product<PK, PK == 3>(kk2[0], kk2[1], a, x);
+                add_product<PK>(kk2[0], kk2[1], a, x);
             }
         }
 #pragma unroll
@@ -556,13 +551,13 @@ delta_grads(const __grid_constant__ GradsArgs p) {
                     rho[half] += pair;
                     col[q] += pair;
                 }
-                uint32_t o[PX], f[PX];
-                split2<PX>(hv[0], hv[1], o);
+                uint32_t o[P], f[P];
+                split2(hv[0], hv[1], o);
 #pragma unroll
-                for (int q = 0; q < PX; ++q) *reinterpret_cast<uint32_t*>(hs + ((q * GT + i) * HP + j) * 2) = o[q];
-                split2<PX>(fv[0], fv[1], f);
+                for (int q = 0; q < P; ++q) *reinterpret_cast<uint32_t*>(hs + ((q * GT + i) * HP + j) * 2) = o[q];
+                split2(fv[0], fv[1], f);
 #pragma unroll
-                for (int q = 0; q < PX; ++q) *reinterpret_cast<uint32_t*>(fs + ((q * GT + i) * HP + j) * 2) = f[q];
+                for (int q = 0; q < P; ++q) *reinterpret_cast<uint32_t*>(fs + ((q * GT + i) * HP + j) * 2) = f[q];
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -622,10 +617,10 @@ delta_grads(const __grid_constant__ GradsArgs p) {
         su[tid] = k;
     }
     for (int jj = 0; jj <= wm; ++jj) {                          // H K, F K
-        uint32_t ah[PX][4], af[PX][4];
+        uint32_t ah[P][4], af[P][4];
         const uint32_t ao = ((wm * 16 + (mi & 1) * 8 + lr) * HP + jj * 16 + (mi >> 1) * 8) * 2;
 #pragma unroll
-        for (int q = 0; q < PX; ++q) {
+        for (int q = 0; q < P; ++q) {
             ldsm4(ah[q], ht + q * GT * HP * 2 + ao);
             ldsm4(af[q], ft + q * GT * HP * 2 + ao);
         }
@@ -635,15 +630,15 @@ delta_grads(const __grid_constant__ GradsArgs p) {
 #pragma unroll
             for (int q = 0; q < PK; ++q)
                 ldsm4t(w[q], kt + ((q * GT + jj * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2);
-            add_product<PX, FX>(fq[2 * n2], fq[2 * n2 + 1], ah, w);
-            add_product<PX, FX>(f5[2 * n2], f5[2 * n2 + 1], af, w);
+            add_product<P>(fq[2 * n2], fq[2 * n2 + 1], ah, w);
+            add_product<P>(f5[2 * n2], f5[2 * n2 + 1], af, w);
         }
     }
     for (int ii = wm; ii < WM; ++ii) {                          // H^T Q, F^T K
-        uint32_t ah[PX][4], af[PX][4];
+        uint32_t ah[P][4], af[P][4];
         const uint32_t ao = ((ii * 16 + (mi >> 1) * 8 + lr) * HP + wm * 16 + (mi & 1) * 8) * 2;
 #pragma unroll
-        for (int q = 0; q < PX; ++q) {
+        for (int q = 0; q < P; ++q) {
             ldsm4t(ah[q], ht + q * GT * HP * 2 + ao);
             ldsm4t(af[q], ft + q * GT * HP * 2 + ao);
         }
@@ -653,10 +648,10 @@ delta_grads(const __grid_constant__ GradsArgs p) {
             const uint32_t bo = ((ii * 16 + (mi & 1) * 8 + lr) * KP + wn * DKW + n2 * 16 + (mi >> 1) * 8) * 2;
 #pragma unroll
             for (int q = 0; q < PK; ++q) ldsm4t(w[q], qt + q * GT * KP * 2 + bo);
-            add_product<PX, FX>(f5[2 * n2], f5[2 * n2 + 1], ah, w);
+            add_product<P>(f5[2 * n2], f5[2 * n2 + 1], ah, w);
 #pragma unroll
             for (int q = 0; q < PK; ++q) ldsm4t(w[q], kt + q * GT * KP * 2 + bo);
-            add_product<PX, FX>(f5[2 * n2], f5[2 * n2 + 1], af, w);
+            add_product<P>(f5[2 * n2], f5[2 * n2 + 1], af, w);
         }
     }
     __syncthreads();
@@ -731,14 +726,14 @@ static ttt_status run_sum_images(const float* part, float* out, int B, long long
     return launch(sum_images, (n + 255) / 256, 256, 0, st, part, out, B, n);
 }
 
-template <int DK, int P, int PK, int RT, int KS>
+template <int DK, int PK, int RT, int KS>
 static ttt_status run_both_t(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const ChainOut& out,
                              const BackOut& bo) {
-    using R = ReverseLayout<DK, P, PK, RT, KS>;
-    using F = ChainLayout<DK, P, PK, RT, KS, true>;
+    using R = ReverseLayout<DK, PK, RT, KS>;
+    using F = ChainLayout<DK, PK, RT, KS, true>;
     constexpr int smem = R::smem > F::smem ? R::smem : F::smem;
     static_assert(smem <= 227 * 1024, "shared memory of a sequential CTA");
-    constexpr auto k = delta_both<DK, P, PK, RT, KS>;
+    constexpr auto k = delta_both<DK, PK, RT, KS>;
     const ttt_status st = allow_smem<k>(std::max(smem, kAloneSmem));
     if (st != TTT_OK) return st;
     const int half = c.d.B * c.d.h * (c.d.dv / (RT * 16));
@@ -747,12 +742,12 @@ static ttt_status run_both_t(const Call& c, const Parts& Q, const Parts& K, cons
                      tiled(O, PK, c.d, c.d.h, c.d.dv, R::VB), rec, c.W0, c.dW1, c.w0_bs, out, bo, error_word(c), c.wait_ns, half};
     return launch(k, 2LL * half, seq_warps<RT, KS>() * 32, spread_smem(smem, 2LL * half, c.sms), c.stream, a);
 }
-template <int DK, int P, int PK>
+template <int DK, int PK>
 static ttt_status run_both(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const ChainOut& out,
                            const BackOut& bo) {
     // fp32: the three parts of a second tile do not fit the shared memory
-    if (PK == 3 || few_tiles(c)) return run_both_t<DK, P, PK, 1, 2>(c, Q, K, O, rec, out, bo);
-    return run_both_t<DK, P, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out, bo);
+    if (PK == 3 || few_tiles(c)) return run_both_t<DK, PK, 1, 2>(c, Q, K, O, rec, out, bo);
+    return run_both_t<DK, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out, bo);
 }
 
 // part: fp32 workspace of the gradients per value head, used where value heads share key heads.

@@ -341,10 +341,10 @@ delta_prep(Dims d, Parts Q, Parts K, View G, View Beta, uint8_t* rec, long long 
 // --------------------------------------------------------------------------------------------------
 // Chain
 // --------------------------------------------------------------------------------------------------
-// A tile is 16 state rows, and two helpers finish it.  With at most one tile per SM a CTA takes one
-// tile, else two, which share the token tiles in shared memory.  2048 tokens, d = 128, forward by one / by two: 144 tiles
-// 106 / 122 us, 192 tiles 197 / 123; backward: 72 tiles 248 / 271, 144 tiles 382 / 359, 256 tiles 690 / 556.
-static bool few_tiles(const Call& c) { return (long long)c.d.B * c.d.h * (c.d.dv / 16) <= c.sms; }
+// A tile is 16 state rows, and two helpers finish it.  With at most one tile per SM (over the sweeps of the launch: one forward, two in the
+// backward pass) a CTA takes one tile, else two, which share the token tiles in shared memory.  2048 tokens, d = 128, forward by one / by
+// two: 144 tiles 106 / 122 us, 192 tiles 197 / 123; backward, tiles of each sweep: 72 248 / 271, 80 308 / 303, 144 382 / 359, 256 690 / 556.
+static bool few_tiles(const Call& c, int sweeps) { return (long long)c.d.B * c.d.h * (c.d.dv / 16) * sweeps <= c.sms; }
 
 struct ChainOut {
     View Z;                       // forward: the readout
@@ -1149,7 +1149,7 @@ static ttt_status forward_t(const Call& c) {
     ChainOut out{};
     out.Z = c.Z;
     out.W1 = c.W1_out;
-    return few_tiles(c) ? run_chain_t<DK, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
+    return few_tiles(c, 1) ? run_chain_t<DK, PK, 1, 2>(c, Q, K, c.ws + l.rec, out) : run_chain_t<DK, PK, 2, 2>(c, Q, K, c.ws + l.rec, out);
 }
 
 template <int DK, int PK>

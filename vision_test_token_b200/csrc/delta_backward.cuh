@@ -746,7 +746,7 @@ template <int DK, int PK>
 static ttt_status run_both(const Call& c, const Parts& Q, const Parts& K, const Parts& O, const uint8_t* rec, const ChainOut& out,
                            const BackOut& bo) {
     // fp32: the three parts of a second tile do not fit the shared memory
-    if (PK == 3 || few_tiles(c)) return run_both_t<DK, PK, 1, 2>(c, Q, K, O, rec, out, bo);
+    if (PK == 3 || few_tiles(c, 2)) return run_both_t<DK, PK, 1, 2>(c, Q, K, O, rec, out, bo);
     return run_both_t<DK, PK, PK == 1 ? 2 : 1, 2>(c, Q, K, O, rec, out, bo);
 }
 
